@@ -73,6 +73,34 @@ class Hybrid(ctypes.Structure):
                 ("cpu_experts", ctypes.c_longlong)]
 
 
+class Router(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int), ("n_group", ctypes.c_int), ("topk_group", ctypes.c_int),
+                ("group_rank", ctypes.c_int), ("renormalize", ctypes.c_int), ("scale", ctypes.c_float),
+                ("bias", ctypes.c_void_p)]
+
+
+class NormArgs(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int), ("H", ctypes.c_int), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+        ("weight", ctypes.c_void_p), ("weight_f32", ctypes.c_int), ("eps", ctypes.c_float),
+        ("residual", ctypes.c_void_p), ("residual_out", ctypes.c_void_p), ("residual_f32", ctypes.c_int),
+        ("ldr", ctypes.c_int64), ("out", ctypes.c_void_p), ("ldo", ctypes.c_int64), ("qmode", ctypes.c_int),
+        ("q", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("q_scale", ctypes.c_void_p),
+    ]
+
+
+class LinearArgs(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int), ("N", ctypes.c_int), ("K", ctypes.c_int), ("qmode", ctypes.c_int),
+        ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("x_scale", ctypes.c_void_p),
+        ("w", ctypes.c_void_p), ("ldw", ctypes.c_int64), ("w_scale", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p), ("fn", ctypes.c_int), ("gated", ctypes.c_int),
+        ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+        ("out", ctypes.c_void_p), ("out_f32", ctypes.c_int), ("ldo", ctypes.c_int64),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 class ExpertCanonical(ctypes.Structure):
     _fields_ = [
         ("fmt", ctypes.c_int32), ("H", ctypes.c_int32), ("I", ctypes.c_int32),
@@ -82,8 +110,14 @@ class ExpertCanonical(ctypes.Structure):
     ]
 
 
+SCORE = {"softmax": 0, "sigmoid": 1}
+GROUP_RANK = {"max": 0, "top2": 1}
+FN = {"none": 0, "silu": 1, "gelu_tanh": 2, "gelu_erf": 3, "relu": 4}
+QMODE = {"none": 0, "fp8": 1, "mxfp8": 2}
+
 # name -> (restype, argtypes); the exported C ABI (include/moe.h)
 _vp, _i, _sz, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+_i64 = ctypes.c_int64
 SIGNATURES = {
     "moe_last_error": (ctypes.c_char_p, []),
     "moe_version": (ctypes.c_char_p, []),
@@ -91,6 +125,8 @@ SIGNATURES = {
     "moe_route": (_i, [_vp, _i, _i, _i, _i, _vp, _vp, _vp]),
     "moe_permute": (_i, [_vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp]),
     "moe_route_permute": (_i, [_vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "moe_route_scored": (_i, [ctypes.POINTER(Router), _vp, _i, _i, _i, _vp, _vp, _vp]),
+    "moe_route_scored_permute": (_i, [ctypes.POINTER(Router), _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "moe_blob_bytes": (_sz, [_i, _i, _i]),
     "moe_prepack_expert": (_i, [ctypes.POINTER(ExpertCanonical), _vp, _sz]),
     "moe_expert_ffn_workspace_size": (_sz, [ctypes.POINTER(FfnArgs)]),
@@ -101,6 +137,10 @@ SIGNATURES = {
     "moe_expert_ffn_traced": (_i, [ctypes.POINTER(FfnArgs), _vp, _vp, _i, _vp]),
     "moe_combine": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp]),
     "moe_quantize_mxfp4": (_i, [_vp, _i, _i, _vp, _vp, _vp]),
+    "moe_rmsnorm": (_i, [ctypes.POINTER(NormArgs), _vp]),
+    "moe_quantize_fp8": (_i, [_vp, _i64, _i, _i, _i, _vp, _vp, _vp]),
+    "moe_linear_workspace_size": (_sz, [ctypes.POINTER(LinearArgs)]),
+    "moe_linear": (_i, [ctypes.POINTER(LinearArgs), _vp]),
     "moe_dequant_blob": (_i, [_vp, _i, _vp, _vp]),
     "moe_debug_fp4_codes": (_i, [ctypes.POINTER(FfnArgs), _i, _vp, _vp, _vp]),
     "moe_cache_create": (_vp, [_i, _sz, _vp, _i, _i]),
@@ -289,6 +329,203 @@ def moe_quantize_mxfp4(x, rows, cols, q, s, stream=None):
 def moe_debug_fp4_codes(args: FfnArgs, which, q, s, stream=None):
     _check(lib().moe_debug_fp4_codes(ctypes.byref(args), int(which), ptr(q), ptr(s), stream_handle(stream)),
            "moe_debug_fp4_codes")
+
+
+# ------------------------------------------------------------ tensor arguments
+# The argument builders below take torch tensors (checked: type, shape, row
+# stride, device) or raw addresses (unchecked, with the sizes given).
+
+_BF16 = ("bfloat16", "int16", "uint16")
+_E4M3 = ("float8_e4m3fn", "uint8")
+_E8M0 = ("float8_e8m0fnu", "uint8")
+_F32 = ("float32",)
+
+
+def _bad(what: str):
+    raise MoeError(MOE_EINVAL, what)
+
+
+class _Taken:
+    """Collects the tensors of one argument struct: the device they share, and references that keep them alive."""
+
+    def __init__(self, who: str):
+        self.who, self.device, self.keep = who, None, []
+
+    def __call__(self, name, t, dtypes, shape):
+        """Address of tensor `t` (None and ints pass) after checking it against the names of its
+        possible types and its shape; the last dimension must be dense."""
+        if t is None or isinstance(t, int):
+            return t
+        who = f"{self.who}: {name}"
+        if str(t.dtype).replace("torch.", "") not in dtypes:
+            _bad(f"{who} is {t.dtype}, expected {' or '.join(dtypes)}")
+        if tuple(t.shape) != tuple(shape):
+            _bad(f"{who} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if not t.is_cuda:
+            _bad(f"{who} is on {t.device}, not on a GPU")
+        if self.device is None:
+            self.device = t.device.index
+        elif t.device.index != self.device:
+            _bad(f"{who} is on {t.device}, other arguments on cuda:{self.device}")
+        self.keep.append(t)
+        return t.data_ptr()
+
+    def dense(self, name, t, dtypes, shape):
+        if t is not None and not isinstance(t, int) and not t.is_contiguous():
+            _bad(f"{self.who}: {name} is not contiguous")
+        return self(name, t, dtypes, shape)
+
+    def rows(self, name, t, dtypes, shape):
+        """(address, row stride in elements) of a [rows, cols] tensor with dense rows."""
+        p = self(name, t, dtypes, shape)
+        if t is None or isinstance(t, int):
+            return p, 0
+        if t.shape[1] > 1 and t.stride(1) != 1:
+            _bad(f"{self.who}: the rows of {name} are not dense (strides {tuple(t.stride())})")
+        if t.shape[0] <= 1:
+            return p, 0
+        if t.stride(0) < t.shape[1]:
+            _bad(f"{self.who}: the rows of {name} overlap (strides {tuple(t.stride())})")
+        return p, t.stride(0)
+
+    def done(self, a):
+        a._keep, a._device = self.keep, self.device
+        return a
+
+
+def _current(a, what: str):
+    """The call's tensors must lie on the current device (its stream runs the kernels)."""
+    d = a.device if isinstance(a, _Taken) else getattr(a, "_device", None)
+    if d is not None:
+        import torch
+        if torch.cuda.current_device() != d:
+            _bad(f"{what}: tensors on cuda:{d}, current device cuda:{torch.cuda.current_device()}")
+
+
+def _is_f32(t, flag):
+    return int(flag) if t is None or isinstance(t, int) else int(str(t.dtype) == "torch.float32")
+
+
+def norm_args(*, x, weight=None, eps=1e-6, residual=None, residual_out=None, out=None, q=None, q_scale=None,
+              qmode="none", T=None, H=None, weight_f32=False, residual_f32=False) -> NormArgs:
+    """Arguments of moe_rmsnorm: x [T,H] bf16; weight [H] and residual [T,H] bf16 or fp32 (taken from
+    the tensors; the flags are for raw addresses); residual_out like residual; out [T,H] bf16; q [T,H]
+    E4M3 codes with q_scale fp32 [T] (qmode "fp8") or E8M0 [H/128, T, 4] (qmode "mxfp8")."""
+    t = _Taken("norm_args")
+    if not isinstance(x, int):
+        if x.dim() != 2:
+            _bad(f"norm_args: x has shape {tuple(x.shape)}, expected [T, H]")
+        T, H = x.shape
+    a = NormArgs()
+    a.T, a.H, a.eps, a.qmode = int(T), int(H), float(eps), QMODE.get(qmode, qmode)
+    a.x, a.ldx = t.rows("x", x, _BF16, (T, H))
+    a.weight, a.weight_f32 = t.dense("weight", weight, _BF16 + _F32, (H,)), _is_f32(weight, weight_f32)
+    a.residual_f32 = _is_f32(residual, residual_f32)
+    rtypes = _F32 if a.residual_f32 else _BF16
+    a.residual, a.ldr = t.rows("residual", residual, rtypes, (T, H))
+    a.residual_out, ldro = t.rows("residual_out", residual_out, rtypes, (T, H))
+    if ldro != a.ldr and residual_out is not None and not isinstance(residual_out, int):
+        _bad("norm_args: residual and residual_out have different row strides")
+    a.out, a.ldo = t.rows("out", out, _BF16, (T, H))
+    a.q, a.ldq = t.rows("q", q, _E4M3, (T, H))
+    if a.qmode == QMODE["mxfp8"]:
+        a.q_scale = t.dense("q_scale", q_scale, _E8M0, (H // 128, T, 4))
+    else:
+        a.q_scale = t.dense("q_scale", q_scale, _F32, (T,))
+    return t.done(a)
+
+
+def router(*, score="softmax", n_group=1, topk_group=1, group_rank="max", renormalize=True, scale=1.0,
+           bias=None) -> Router:
+    """A router for moe_route_scored: score "softmax" or "sigmoid", n_group groups of which the topk_group best
+    by group_rank ("max" or "top2") are kept, bias [E] fp32 (device) for the choice alone."""
+    t = _Taken("router")
+    r = Router()
+    r.score, r.group_rank = SCORE.get(score, score), GROUP_RANK.get(group_rank, group_rank)
+    r.n_group, r.topk_group, r.renormalize, r.scale = int(n_group), int(topk_group), int(renormalize), float(scale)
+    r._experts = None if bias is None or isinstance(bias, int) else bias.numel()
+    r.bias = t.dense("bias", bias, _F32, (r._experts,))
+    return t.done(r)
+
+
+def _check_router(r: Router, E: int, what: str):
+    n = getattr(r, "_experts", None)
+    if n is not None and n != E:
+        _bad(f"{what}: the router's bias has {n} experts, E={E}")
+    _current(r, what)
+
+
+def moe_route_scored(r: Router, logits, T, E, k, topk_ids, topk_w, stream=None):
+    _check_router(r, E, "moe_route_scored")
+    _check(lib().moe_route_scored(ctypes.byref(r), ptr(logits), T, E, k, ptr(topk_ids), ptr(topk_w),
+                                  stream_handle(stream)), "moe_route_scored")
+
+
+def moe_route_scored_permute(r: Router, logits, T, E, k, topk_ids, topk_w, counts, offsets, perm, inv, stream=None):
+    _check_router(r, E, "moe_route_scored_permute")
+    _check(lib().moe_route_scored_permute(ctypes.byref(r), ptr(logits), T, E, k, ptr(topk_ids), ptr(topk_w),
+                                          ptr(counts), ptr(offsets), ptr(perm), ptr(inv), stream_handle(stream)),
+           "moe_route_scored_permute")
+
+
+def moe_rmsnorm(args: NormArgs, stream=None):
+    _current(args, "moe_rmsnorm")
+    _check(lib().moe_rmsnorm(ctypes.byref(args), stream_handle(stream)), "moe_rmsnorm")
+
+
+def moe_quantize_fp8(x, rows, cols, qmode, q, q_scale, stream=None, ldx=0):
+    """8-bit rows of bf16 x [rows, cols] (tensor: its own row stride; raw address: ldx elements, 0 dense):
+    dense E4M3 codes q [rows, cols], q_scale fp32 [rows] (qmode "fp8") or E8M0 [cols/128, rows, 4] ("mxfp8")."""
+    t, qm = _Taken("moe_quantize_fp8"), QMODE.get(qmode, qmode)
+    xp, ld = t.rows("x", x, _BF16, (rows, cols))
+    qp = t.dense("q", q, _E4M3, (rows, cols))
+    sp = (t.dense("q_scale", q_scale, _E8M0, (cols // 128, rows, 4)) if qm == QMODE["mxfp8"] else
+          t.dense("q_scale", q_scale, _F32, (rows,)))
+    _current(t, "moe_quantize_fp8")
+    _check(lib().moe_quantize_fp8(xp, ld or ldx, rows, cols, qm, qp, sp, stream_handle(stream)), "moe_quantize_fp8")
+
+
+def linear_args(*, x, w, out, fmt="bf16", x_scale=None, w_scale=None, bias=None, act="none", gated=False,
+                residual=None, T=None, N=None, K=None, out_f32=False) -> LinearArgs:
+    """Arguments of moe_linear (workspace left empty): x [T,K] and w [R,K] bf16 (fmt "bf16") or E4M3 codes with
+    x_scale / w_scale (fmt "fp8": fp32 [T] / [R]; "mxfp8": E8M0 [K/128, T, 4] / [K/128, R, 4]); R = N, gated 2 N;
+    bias fp32 [R]; residual [T,N] bf16; out [T,N] bf16 or fp32."""
+    t = _Taken("linear_args")
+    for name, v in (("x", x), ("w", w), ("out", out)):
+        if not isinstance(v, int) and v.dim() != 2:
+            _bad(f"linear_args: {name} has shape {tuple(v.shape)}, expected two dimensions")
+    if not isinstance(x, int):
+        T, K = x.shape
+    if not isinstance(out, int):
+        N = out.shape[1]
+    R = 2 * N if gated else N
+    a = LinearArgs()
+    a.T, a.N, a.K, a.gated = int(T), int(N), int(K), int(gated)
+    a.qmode = QMODE["none"] if fmt == "bf16" else QMODE.get(fmt, fmt)
+    a.fn = FN.get(act, act)
+    types = _BF16 if a.qmode == QMODE["none"] else _E4M3
+    a.x, a.ldx = t.rows("x", x, types, (T, K))
+    a.w, a.ldw = t.rows("w", w, types, (R, K))
+    if a.qmode == QMODE["mxfp8"]:
+        a.x_scale = t.dense("x_scale", x_scale, _E8M0, (K // 128, T, 4))
+        a.w_scale = t.dense("w_scale", w_scale, _E8M0, (K // 128, R, 4))
+    else:
+        a.x_scale = t.dense("x_scale", x_scale, _F32, (T,))
+        a.w_scale = t.dense("w_scale", w_scale, _F32, (R,))
+    a.bias = t.dense("bias", bias, _F32, (R,))
+    a.residual, a.ldr = t.rows("residual", residual, _BF16, (T, N))
+    a.out_f32 = _is_f32(out, out_f32)
+    a.out, a.ldo = t.rows("out", out, _F32 if a.out_f32 else _BF16, (T, N))
+    return t.done(a)
+
+
+def moe_linear_workspace_size(args: LinearArgs) -> int:
+    return int(lib().moe_linear_workspace_size(ctypes.byref(args)))
+
+
+def moe_linear(args: LinearArgs, stream=None):
+    _current(args, "moe_linear")
+    _check(lib().moe_linear(ctypes.byref(args), stream_handle(stream)), "moe_linear")
 
 
 def moe_dequant_blob(blob, which, out, stream=None):

@@ -103,6 +103,46 @@ moe_status moe_route_permute(const float* logits, int T, int E, int k, int renor
                              float* topk_w, int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv,
                              moe_stream_t stream);
 
+/* Scored routing: scores other than the plain softmax, a bias that balances
+ * the experts' load, and groups of experts.
+ * [pages as for moe_route; the rule below is this library's reading.] */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_rank;
+
+typedef struct {
+  int score;          /* moe_score: s_e = softmax(l)_e over all E, or 1 / (1 + exp(-l_e)) */
+  int n_group;        /* the E experts in n_group groups of E / n_group consecutive ids;
+                         1: no groups.  n_group <= 64, E % n_group == 0                */
+  int topk_group;     /* groups whose experts may be taken, 1 <= topk_group <= n_group  */
+  int group_rank;     /* moe_group_rank: a group's rank is its largest key, or the sum
+                         of its two largest (of its only one if it has one)            */
+  int renormalize;    /* weights divided by their sum over the k selected               */
+  float scale;        /* factor of every weight, applied last                           */
+  const float* bias;  /* nullable, device [E] fp32: added to the scores for the choice
+                         alone, never to the weights; -inf keeps an expert behind every
+                         other                                                         */
+} moe_router;
+
+/* moe_route by a moe_router.  The choice: key_e = s_e + bias_e, and without
+ * a bias the logit itself, which has the scores' order; with groups, only the
+ * experts of the topk_group best groups (MOE_GROUP_TOP2 without a bias sums
+ * scores); then the k largest keys, in rank order.  Equal keys and equal
+ * groups: the lower id first.  A NaN key ranks below -inf, and counts as -inf
+ * in a group's sum.  Keys that lie too close for fp32 are compared as the
+ * formulas give them in 64 bits.
+ * The weights: w_j = s_j (NaN logits: 0; -inf logits under sigmoid: 0), with
+ * renormalize divided by their sum over the k selected; a row whose weights
+ * would all be 0 by a zero sum gets 1/k each; all times scale.
+ * Requires 1 <= k <= min(topk_group * (E / n_group), 16), E <= 1024, T >= 0. */
+moe_status moe_route_scored(const moe_router* r, const float* logits, int T, int E, int k, int32_t* topk_ids,
+                            float* topk_w, moe_stream_t stream);
+
+/* moe_route_scored followed by the permutation of moe_permute, in as few
+ * launches as the batch allows.  Requires T*k <= 131072 too. */
+moe_status moe_route_scored_permute(const moe_router* r, const float* logits, int T, int E, int k, int32_t* topk_ids,
+                                    float* topk_w, int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv,
+                                    moe_stream_t stream);
+
 /* ------------------------------------------------------------- expert FFN */
 
 /* Prepacked expert ("slot blob") layout, shared by the host bank and the HBM
@@ -260,6 +300,117 @@ moe_status moe_combine(const float* y, const int32_t* inv, const float* topk_w, 
  * s: [rows, cols/32] E8M0.  cols % 32 == 0. */
 moe_status moe_quantize_mxfp4(const uint16_t* x, int rows, int cols, uint8_t* q, uint8_t* s,
                               moe_stream_t stream);
+
+/* --------------------------------------------------- norm and 8-bit rows
+ * [bhrtaym-blog page, section on models and quantisation formats: FP8 among
+ *  the formats; the norm in front of a layer, its residual and the encodings
+ *  are this library's reading.] */
+
+/* 8-bit row encodings: E4M3FN codes (element c of a row at byte c) and scales.
+ *   MOE_Q_FP8:   one fp32 scale a row, s = max(amax / 448, 2^-126).
+ *   MOE_Q_MXFP8: one E8M0 scale per 32 columns, 2^(floor(log2 amax) - 8)
+ *                (code 127 for an all-zero block, at least 0 and at most 254),
+ *                stored K-tile-major: byte j of [cols / 128][rows][4] is the
+ *                scale of columns 128 kt + 32 j .. + 31 (kt the first index),
+ *                the order in which moe_linear reads them.  cols % 128 == 0.
+ * A code is value / scale rounded to nearest even, saturating at +-448; a
+ * NaN value stays NaN (0x7F or 0xFF) and counts for no maximum.  With an
+ * infinite value the fp32 scale is infinite (that value's code NaN, the
+ * others 0), the E8M0 code 247 (that value +-448). */
+typedef enum { MOE_Q_NONE = 0, MOE_Q_FP8 = 1, MOE_Q_MXFP8 = 2 } moe_qmode;
+
+/* Arguments of moe_rmsnorm.  Row strides are in elements, at least H, a
+ * multiple of 8, and 0 means H; every pointer 16-byte aligned (q and scales:
+ * 8).  Rows of H elements; what lies between a row's end and the next row's
+ * start is neither read nor written. */
+typedef struct {
+  int T, H;                 /* tokens, hidden; H % 8 == 0, 8 <= H <= 32768           */
+  const uint16_t* x;        /* [T,H] bf16                                            */
+  int64_t ldx;
+  const void* weight;       /* nullable (1): [H] bf16, or fp32 with weight_f32       */
+  int weight_f32;
+  float eps;                /* >= 0                                                  */
+  const void* residual;     /* nullable: [T,H] bf16, or fp32 with residual_f32       */
+  void* residual_out;       /* nullable: [T,H] of residual's type and stride: x +
+                               residual; may be residual itself                      */
+  int residual_f32;
+  int64_t ldr;
+  uint16_t* out;            /* nullable: [T,H] bf16; may be x itself (same stride)   */
+  int64_t ldo;
+  int qmode;                /* moe_qmode: the 8-bit output                           */
+  uint8_t* q;               /* [T,H] codes (required unless MOE_Q_NONE)              */
+  int64_t ldq;
+  void* q_scale;            /* fp32 [T], or E8M0 [H/128][T][4]                       */
+} moe_norm_args;
+
+/* RMS norm of x + residual over each row, in one pass over the data:
+ *   r = x + residual (fp32; residual_out is r rounded once),
+ *   y = r * weight / sqrt(mean(r^2) + eps)   (from the unrounded r),
+ * written as bf16 (out) and as 8-bit rows (q, q_scale), both rounded from
+ * the fp32 y.  One of out, q and residual_out at least.
+ * Errors: MOE_EINVAL (sizes, strides, null or misaligned pointers);
+ * nothing is enqueued on an error. */
+moe_status moe_rmsnorm(const moe_norm_args* a, moe_stream_t stream);
+
+/* The 8-bit encoding alone: q, q_scale of the bf16 rows x [rows, cols]
+ * (row stride ldx, 0 for cols; q dense), by moe_rmsnorm's kernel without the
+ * norm: the operand of a moe_linear whose input is another product's output.
+ * cols as H above. */
+moe_status moe_quantize_fp8(const uint16_t* x, int64_t ldx, int rows, int cols, int qmode, uint8_t* q, void* q_scale,
+                            moe_stream_t stream);
+
+/* -------------------------------------------------------- linear product */
+
+typedef enum {
+  MOE_FN_NONE = 0,
+  MOE_FN_SILU = 1,      /* z / (1 + exp(-z))                                            */
+  MOE_FN_GELU_TANH = 2, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2            */
+  MOE_FN_GELU_ERF = 3,  /* z (1 + erf(z / sqrt 2)) / 2                                  */
+  MOE_FN_RELU = 4       /* max(z, 0), NaN kept                                          */
+} moe_fn;
+
+/* Arguments of moe_linear.  Row strides are in elements, 0 means dense.
+ * x and w rows: K bf16 values (qmode MOE_Q_NONE) or E4M3 codes with the
+ * scales of their encoding (MOE_Q_FP8: fp32 [T] and [R]; MOE_Q_MXFP8: E8M0
+ * [K/128][T][4] and [K/128][R][4]), R = N, or 2 N with gated. */
+typedef struct {
+  int T, N, K;              /* rows of x, columns of out, contraction                  */
+  int qmode;                /* moe_qmode of x and w                                    */
+  const void* x;            /* [T,K]                                                   */
+  int64_t ldx;
+  const void* x_scale;
+  const void* w;            /* [R,K]; gated: the N gate rows, then the N up rows       */
+  int64_t ldw;
+  const void* w_scale;
+  const float* bias;        /* nullable: [R] fp32                                      */
+  int fn;                   /* moe_fn                                                  */
+  int gated;                /* out = fn(gate) * up (+ residual)                        */
+  const uint16_t* residual; /* nullable: [T,N] bf16; may be out itself (bf16, same stride) */
+  int64_t ldr;
+  void* out;                /* [T,N] bf16, or fp32 with out_f32                        */
+  int out_f32;
+  int64_t ldo;
+  void* workspace;          /* device scratch, >= moe_linear_workspace_size, 16-byte
+                               aligned; no contents carry over between calls.  Calls
+                               that share a workspace must not overlap.                */
+  size_t workspace_bytes;
+} moe_linear_args;
+
+/* Bytes of device workspace a call with these dimensions needs (0: none; the
+ * pointers need not be set). */
+size_t moe_linear_workspace_size(const moe_linear_args* a);
+
+/* out = fn(x W^T + bias) + residual, or fn(x W_g^T + b_g) * (x W_u^T + b_u) +
+ * residual: products of the exact operands summed in fp32, the epilogue in
+ * fp32, one rounding to out's type.
+ * [page "FreeToken qwen：...", 3rd paragraph: the layer's products; the dense
+ *  product beside the experts and its epilogue are this library's reading.]
+ * Requires T >= 0, N >= 1, K >= 1, rows of whole 16-byte pieces (K % 8 == 0
+ * for bf16, K % 16 == 0 for FP8, K % 128 == 0 for MXFP8; strides alike, at
+ * least the row), x and w on 16-byte boundaries, N and T below 2^24.
+ * Errors: MOE_EINVAL, MOE_ENOMEM (workspace too small); nothing is enqueued
+ * on an error. */
+moe_status moe_linear(const moe_linear_args* a, moe_stream_t stream);
 
 /* Debug: the MXFP4 encodings an FP4 matrix-core call (amode MXFP4) left in
  * its workspace, copied to canonical layout, for the bit-exact tests of the
