@@ -53,15 +53,18 @@ __global__ __launch_bounds__(64 * WM* WN) __attribute__((amdgpu_waves_per_eu(2, 
   constexpr int CA = BM / 8 / NW, CB = BN / 8 / NW;  // 1 KiB loads a wave and step
   constexpr bool MX = QM == MOE_Q_MXFP8;
   constexpr int SC = (BM + BN) / 64;                 // 64-row scale pieces
-  constexpr int kScaleOff = (BM + BN) * 128;
-  constexpr int kStage = kScaleOff + (MX ? (BM + BN) * 4 : 0);
-  constexpr int kLoads = CA + CB + (MX ? 1 : 0);
+  constexpr int kStage = (BM + BN) * 128;
+  constexpr int kScales = MX ? (BM + BN) * 4 : 0;    // a step's scales, in a ring of S + 1
+  constexpr int kWait = (S - 1) * (CA + CB + (MX ? 1 : 0));  // loads of S - 1 steps
+  constexpr int TH = TM / 2;
   constexpr int OC = GATED ? TN / 2 : TN;            // 16-column groups of output a wave
   constexpr int BO = GATED ? BN / 2 : BN;            // output columns a tile
   constexpr int SR = OC * 16 + 4;                    // staging row, floats
-  static_assert(CA * 8 * NW == BM && CB * 8 * NW == BN && SC <= NW && TN % 2 == 0, "tile shape");
+  static_assert(CA * 8 * NW == BM && CB * 8 * NW == BN && SC <= NW && TN % 2 == 0 && CA % 2 == 0, "tile shape");
+  static_assert(!MX || (BM % 64 == 0 && BN % 64 == 0), "whole scale pieces");
   static_assert(NW * 16 * SR * 4 <= S * kStage, "staging fits the ring");
   __shared__ __align__(1024) uint8_t ring[S * kStage];
+  __shared__ __align__(256) uint8_t s_mx[MX ? (S + 1) * kScales : 16];
   __shared__ __align__(16) float s_ws[BN], s_bias[BN], s_xs[BM];  // scales and bias of the tile's rows
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -79,6 +82,7 @@ __global__ __launch_bounds__(64 * WM* WN) __attribute__((amdgpu_waves_per_eu(2, 
   const int t0 = (4 * band + in_band % bh) * BM, n0 = (in_band / bh) * BO;
 
   const uint32_t ring0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)ring;
+  const uint32_t mx0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)s_mx;
   const int steps = (P.kb + 127) / 128;
   const int tail = MX ? 0 : P.kb & 127;  // bytes of a partial last step, 0: none
 
@@ -88,9 +92,15 @@ __global__ __launch_bounds__(64 * WM* WN) __attribute__((amdgpu_waves_per_eu(2, 
   uint32_t aoff[CA], boff[CB];
   const int lr = lane >> 3;
   auto piece = [&](int c) { return (lane & 7) ^ ((4 * (c & 1) + (lr >> 1)) & 7); };
+  // A chunk u of this wave: the first CA / 2 hold rows of the waves' first
+  // TH tiles, the others rows of the second
+  auto a_chunk = [&](int u) {
+    const int h = u / (CA / 2), n = wave * (CA / 2) + u % (CA / 2);
+    return n / (2 * TH) * (2 * TM) + n % (2 * TH) + h * 2 * TH;
+  };
 #pragma unroll
   for (int u = 0; u < CA; ++u) {
-    const int c = wave * CA + u;
+    const int c = a_chunk(u);
     aoff[u] = (uint32_t)min(8 * c + lr, P.T - 1 - t0) * (uint32_t)P.ldx + piece(c) * 16;
   }
 #pragma unroll
@@ -119,30 +129,52 @@ __global__ __launch_bounds__(64 * WM* WN) __attribute__((amdgpu_waves_per_eu(2, 
   }
   const int64_t up = GATED ? (int64_t)P.N * P.ldw : 0;
   // a partial step's pieces past the row's end re-read its last piece
-  uint32_t back[2];
-#pragma unroll
-  for (int c = 0; c < 2; ++c) back[c] = tail != 0 ? (uint32_t)max(piece(c) * 16 - (tail - 16), 0) : 0u;
-  // Step s into stage s % S; past the end the last step again (the counted
-  // waits need the same number of loads every step).
-  auto issue = [&](int s) __attribute__((always_inline)) {
-    const uint32_t st = ring0 + (uint32_t)(s % S) * kStage;
-    const int sl = min(s, steps - 1);
-    const uint32_t cut = sl == steps - 1 ? ~0u : 0u;
-    const uint32_t b0 = back[0] & cut, b1 = back[1] & cut;
-    const uint8_t* ab = abase + (int64_t)sl * 128;
-    const uint8_t* bb = bbase + (int64_t)sl * 128;
-#pragma unroll
-    for (int u = 0; u < CA; ++u) {
-      const int c = wave * CA + u;
-      dma16s(aoff[u] - (CA % 2 == 0 ? (u & 1 ? b1 : b0) : (c & 1 ? b1 : b0)), ab, st + c * 1024);
+  const uint32_t back0 = tail != 0 ? (uint32_t)max(piece(0) * 16 - (tail - 16), 0) : 0u;  // even chunks
+  const uint32_t back1 = tail != 0 ? (uint32_t)max(piece(1) * 16 - (tail - 16), 0) : 0u;  // odd chunks
+  // The load side: step f goes to the stage at ring offset `fill`, in two
+  // parts: the weights, the scales and the first half of x; the second half
+  // of x.  Past the end the last step again (the counted waits need the same
+  // number of loads every step).  Running pointers and offsets: products and
+  // remainders of the step number would stand in every wave's way.
+  const uint8_t *pa = abase, *pb = bbase, *ps = sbase;
+  uint32_t cut = steps == 1 ? ~0u : 0u;  // all ones from the last step on
+  uint32_t fill = 0, fill_mx = 0;
+  int f = 0;
+  auto load_a = [&](int u) __attribute__((always_inline)) {
+    const int c = a_chunk(u);
+    dma16s(aoff[u] - ((c & 1 ? back1 : back0) & cut), pa, ring0 + fill + c * 1024);
+  };
+  // load k of part 1
+  constexpr int kPart1 = CB + CA / 2 + (MX ? 1 : 0);
+  auto load1 = [&](int k) __attribute__((always_inline)) {
+    if (k < CB) {
+      const int c = wave * CB + k;
+      dma16s(boff[k < CB ? k : 0] - ((c & 1 ? back1 : back0) & cut), pb + (GATED && ((c >> 1) & 1) ? up : 0),
+             ring0 + fill + BM * 128 + c * 1024);
+    } else if (k < CB + CA / 2) {
+      load_a(k - CB);
+    } else if (MX && k == CB + CA / 2) {
+      dma4s(soff, ps, mx0 + fill_mx + sc * 256);
     }
-#pragma unroll
-    for (int u = 0; u < CB; ++u) {
-      const int c = wave * CB + u;
-      dma16s(boff[u] - (CB % 2 == 0 ? (u & 1 ? b1 : b0) : (c & 1 ? b1 : b0)), bb + (GATED && ((c >> 1) & 1) ? up : 0),
-             st + BM * 128 + c * 1024);
+  };
+  // after both parts of a step
+  auto filled = [&]() __attribute__((always_inline)) {
+    ++f;
+    if (f < steps) {
+      pa += 128;
+      pb += 128;
+      if constexpr (MX) ps += sstep;
     }
-    if constexpr (MX) dma4s(soff, sbase + sl * sstep, st + kScaleOff + sc * 256);
+    cut = f >= steps - 1 ? ~0u : 0u;
+    if constexpr (MX) fill_mx = fill_mx == S * kScales ? 0 : fill_mx + kScales;
+    fill = fill == (S - 1) * kStage ? 0 : fill + kStage;
+  };
+  auto issue = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < kPart1; ++k) load1(k);
+#pragma unroll
+    for (int u = CA / 2; u < CA; ++u) load_a(u);
+    filled();
   };
 
   lf32x4_t acc[TM][TN];
@@ -155,7 +187,7 @@ __global__ __launch_bounds__(64 * WM* WN) __attribute__((amdgpu_waves_per_eu(2, 
   const uint32_t rd = r16 * 128 + ((g ^ (r16 >> 1)) << 4);
   const uint32_t rda = wm * TM * 2048 + rd, rdb = BM * 128 + wn * TN * 2048 + rd;
   const uint32_t rda4 = rda ^ 64, rdb4 = rdb ^ 64;
-  const uint32_t rsa = kScaleOff + (wm * TM * 16 + r16) * 4, rsb = kScaleOff + (BM + wn * TN * 16 + r16) * 4;
+  const uint32_t rsa = (wm * TM * 16 + r16) * 4, rsb = (BM + wn * TN * 16 + r16) * 4;
 
   auto frag = [&](const uint8_t* p, const uint8_t* p4) __attribute__((always_inline)) {
     Frag f;
@@ -167,7 +199,6 @@ __global__ __launch_bounds__(64 * WM* WN) __attribute__((amdgpu_waves_per_eu(2, 
   // takes one byte of a register (its number a constant), so the scales of a
   // half's fragments share one.  EXACT: lane's pieces g and 4 + g lie in
   // blocks g / 2 and 2 + g / 2 of the step's four.
-  constexpr int TH = TM / 2;
   static_assert(TH <= 4 && TN <= 4, "scale bytes of a half");
   Frag fw[TN], fx[TM];
   int sw = 0x7F7F7F7F, sx[2] = {0x7F7F7F7F, 0x7F7F7F7F};            // MX
@@ -200,16 +231,16 @@ __global__ __launch_bounds__(64 * WM* WN) __attribute__((amdgpu_waves_per_eu(2, 
     acc[i][j] = c;
   };
   // Fragments of the step in work; the halves of fx are read half a step apart.
-  auto read_w = [&](const uint8_t* st, int j) __attribute__((always_inline)) {
-    if constexpr (MX && EXACT) ew[j] = *reinterpret_cast<const uint32_t*>(st + rsb + j * 64);
-    if constexpr (MX && !EXACT) rw[j] = st[rsb + g + j * 64];
+  auto read_w = [&](const uint8_t* st, const uint8_t* mx, int j) __attribute__((always_inline)) {
+    if constexpr (MX && EXACT) ew[j] = *reinterpret_cast<const uint32_t*>(mx + rsb + j * 64);
+    if constexpr (MX && !EXACT) rw[j] = mx[rsb + g + j * 64];
     fw[j] = frag(st + rdb + j * 2048, st + rdb4 + j * 2048);
   };
-  auto read_x = [&](const uint8_t* st, int half) __attribute__((always_inline)) {
+  auto read_x = [&](const uint8_t* st, const uint8_t* mx, int half) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < TH; ++i) {
-      if constexpr (MX && EXACT) ex[half * TH + i] = *reinterpret_cast<const uint32_t*>(st + rsa + (half * TH + i) * 64);
-      if constexpr (MX && !EXACT) rx[i] = st[rsa + g + (half * TH + i) * 64];
+      if constexpr (MX && EXACT) ex[half * TH + i] = *reinterpret_cast<const uint32_t*>(mx + rsa + (half * TH + i) * 64);
+      if constexpr (MX && !EXACT) rx[i] = mx[rsa + g + (half * TH + i) * 64];
     }
 #pragma unroll
     for (int i = half * TH; i < (half + 1) * TH; ++i)
@@ -222,15 +253,39 @@ __global__ __launch_bounds__(64 * WM* WN) __attribute__((amdgpu_waves_per_eu(2, 
     for (int i = 1; i < n; ++i) p |= r[i] << (8 * i);
     return (int)p;
   };
+  // Fragment j of the weights against half h of x.  S = 2: part 1 of step s
+  // is loaded beside the first half, part 2 beside the second, spread between
+  // the matrix instructions: issued together they would hold back every
+  // wave's instructions behind the texture unit (76 -> 73 us, 95 -> 92 us at
+  // the FP8 and MXFP8 prefills).
   auto mma_j = [&](auto jc, auto hc) __attribute__((always_inline)) {
-    constexpr int h = decltype(hc)::value;
-    mma(jc, std::integral_constant<int, h * TH>{});
-    if constexpr (TH > 1) mma(jc, std::integral_constant<int, h * TH + 1 % TH>{});
-    if constexpr (TH > 2) mma(jc, std::integral_constant<int, h * TH + 2 % TH>{});
-    if constexpr (TH > 3) mma(jc, std::integral_constant<int, h * TH + 3 % TH>{});
+    constexpr int j = decltype(jc)::value, h = decltype(hc)::value;
+    constexpr int from = S == 2 && h == 1 ? kPart1 : 0;           // loads [from, to) beside this half
+    constexpr int to = S > 2 ? 0 : (h == 0 ? kPart1 : kPart1 + CA / 2);
+    constexpr int slots = TN * TH;
+    auto one = [&](auto ic) __attribute__((always_inline)) {
+      constexpr int i = decltype(ic)::value, at = j * TH + i;
+      mma(jc, std::integral_constant<int, h * TH + i>{});
+      constexpr int k0 = from + (to - from) * at / slots, k1 = from + (to - from) * (at + 1) / slots;
+      if constexpr (k1 > k0) {
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int k = k0; k < k1; ++k) {
+          if (k < kPart1) load1(k);
+          else load_a(CA / 2 + k - kPart1);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    one(std::integral_constant<int, 0>{});
+    if constexpr (TH > 1) one(std::integral_constant<int, 1>{});
+    if constexpr (TH > 2) one(std::integral_constant<int, 2>{});
+    if constexpr (TH > 3) one(std::integral_constant<int, 3>{});
   };
   // the pieces of a partial step past the rows' end: zero
   auto zero_tail = [&](uint8_t* st) __attribute__((always_inline)) {
+    wait_loads<0>();
+    lds_sync();
     for (int i = tid; i < (BM + BN) * 8; i += 64 * NW) {
       const int row = i >> 3, pc = (i & 7) ^ ((row >> 1) & 7);
       if (pc * 16 >= tail) *reinterpret_cast<uint4*>(st + i * 16) = make_uint4(0, 0, 0, 0);
@@ -246,7 +301,7 @@ __global__ __launch_bounds__(64 * WM* WN) __attribute__((amdgpu_waves_per_eu(2, 
   };
 
 #pragma unroll
-  for (int s = 0; s < S; ++s) issue(s);
+  for (int s = 0; s < S; ++s) issue();
   for (int i = tid; i < BN; i += 64 * NW) {
     const int col = min(n0 + (GATED ? (i >> 5) * 16 + (i & 15) : i), P.N - 1) + (GATED && ((i >> 4) & 1) ? P.N : 0);
     if constexpr (QM == MOE_Q_FP8) s_ws[i] = static_cast<const float*>(P.ws)[col];
@@ -254,12 +309,12 @@ __global__ __launch_bounds__(64 * WM* WN) __attribute__((amdgpu_waves_per_eu(2, 
   }
   if constexpr (QM == MOE_Q_FP8)
     for (int i = tid; i < BM; i += 64 * NW) s_xs[i] = static_cast<const float*>(P.xs)[min(t0 + i, P.T - 1)];
-  wait_loads<(S - 1) * kLoads>();
+  wait_loads<kWait>();
   lds_sync();
   if (!MX && tail != 0 && steps == 1) zero_tail(ring);
 #pragma unroll
-  for (int j = 0; j < TN; ++j) read_w(ring, j);
-  read_x(ring, 0);
+  for (int j = 0; j < TN; ++j) read_w(ring, s_mx, j);
+  read_x(ring, s_mx, 0);
   if constexpr (MX && !EXACT) {
     sw = pack(rw, TN);
     sx[0] = pack(rx, TH);
@@ -268,15 +323,30 @@ __global__ __launch_bounds__(64 * WM* WN) __attribute__((amdgpu_waves_per_eu(2, 
   using I1 = std::integral_constant<int, 1>;
   using I2 = std::integral_constant<int, 2 % TN>;
   using I3 = std::integral_constant<int, 3 % TN>;
-  // Step s.  First half: tokens 0 .. TH - 1 of the wave's tiles, while the
-  // other tokens' fragments are read.  Then every wave has read the whole
-  // stage, which takes step s + S, and stage s + 1 has landed.  Second half:
-  // the other tokens, while step s + 1's fragments replace those used up.
+  // Step s, whose weights and first half of x are in registers.  First half:
+  // tokens 0 .. TH - 1 of the wave's tiles, while the other tokens' fragments
+  // are read.  Second half: the other tokens, while step s + 1's fragments
+  // replace those used up.  Before the second half every wave has read the
+  // whole stage.  S = 2: part 1 of step s + 2 already refills, beside the
+  // first half, what every wave had read by then, at the price of a second
+  // barrier, so that a load has a step and a half to land; with S = 3 two
+  // steps are in flight, and one barrier with the loads right behind it is
+  // faster (4096 x 2048 x 2048 bf16, 128 x 256 tiles: 36 against 44 us; loads
+  // spread between the matrix instructions 41).
+  uint32_t at = 0, at_mx = 0;  // stage of step s
 #pragma unroll 1
   for (int s = 0; s < steps; ++s) {
-    const uint8_t* st = ring + (s % S) * kStage;
-    uint8_t* nx = ring + ((s + 1) % S) * kStage;
-    read_x(st, 1);
+    const uint8_t* st = ring + at;
+    const uint8_t* mx = s_mx + at_mx;
+    at = at == (S - 1) * kStage ? 0 : at + kStage;
+    if constexpr (MX) at_mx = at_mx == S * kScales ? 0 : at_mx + kScales;
+    uint8_t* nx = ring + at;
+    const uint8_t* mxn = s_mx + at_mx;
+    if constexpr (S == 2) {
+      wait_loads<kWait>();  // part 2 of step s
+      lds_sync();
+    }
+    read_x(st, mx, 1);
     __builtin_amdgcn_sched_barrier(0);
     mma_j(I0{}, I0{});
     mma_j(I1{}, I0{});
@@ -284,22 +354,23 @@ __global__ __launch_bounds__(64 * WM* WN) __attribute__((amdgpu_waves_per_eu(2, 
     if constexpr (TN > 3) mma_j(I3{}, I0{});
     pin(0, TH);
     if constexpr (MX && !EXACT) sx[1] = pack(rx, TH);
-    wait_loads<(S - 2) * kLoads>();
+    wait_loads<S == 2 ? kWait : kWait - kWait / (S - 1)>();  // S = 2: part 1 of step s + 1; else both parts
     lds_sync();
     if (!MX && tail != 0 && s == steps - 2) zero_tail(nx);
-    issue(s + S);
-    read_x(nx, 0);
+    if constexpr (S > 2) issue();
+    read_x(nx, mxn, 0);
     auto second = [&](auto jc) __attribute__((always_inline)) {
       __builtin_amdgcn_sched_barrier(0);
       mma_j(jc, I1{});
       __builtin_amdgcn_sched_barrier(0);
-      read_w(nx, decltype(jc)::value);
+      read_w(nx, mxn, decltype(jc)::value);
     };
     second(I0{});
     second(I1{});
     if constexpr (TN > 2) second(I2{});
     if constexpr (TN > 3) second(I3{});
     pin(TH, TM);
+    if constexpr (S == 2) filled();
     if constexpr (MX && !EXACT) {
       sw = pack(rw, TN);
       sx[0] = pack(rx, TH);
