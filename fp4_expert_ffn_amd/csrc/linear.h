@@ -41,21 +41,42 @@ __device__ __forceinline__ lf32x4_t mma_bf16(lbf16x8_t w, lbf16x8_t x, lf32x4_t 
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x, c, 0, 0, 0);
 }
 
-// One K-step, every product exact and every sum in fp32.  E4M3 operands are
-// decoded to bf16 first: the FP8 matrix instructions add 8 neighbouring
-// products after cutting each below 2^-13 of the largest of them (measured
-// on the GPU), which an fp32 output would show.
-template <int QM>
-__device__ __forceinline__ lf32x4_t mma_exact(const Frag& w, const Frag& x, lf32x4_t c, float fw, float fx) {
-  if constexpr (QM == MOE_Q_NONE) {
-    c = mma_bf16(__builtin_bit_cast(lbf16x8_t, w.a), __builtin_bit_cast(lbf16x8_t, x.a), c);
-    return mma_bf16(__builtin_bit_cast(lbf16x8_t, w.b), __builtin_bit_cast(lbf16x8_t, x.b), c);
-  } else {
-    c = mma_bf16(e4m3_bf16(w.a.x, w.a.y, fw), e4m3_bf16(x.a.x, x.a.y, fx), c);
-    c = mma_bf16(e4m3_bf16(w.a.z, w.a.w, fw), e4m3_bf16(x.a.z, x.a.w, fx), c);
-    c = mma_bf16(e4m3_bf16(w.b.x, w.b.y, fw), e4m3_bf16(x.b.x, x.b.y, fx), c);
-    return mma_bf16(e4m3_bf16(w.b.z, w.b.w, fw), e4m3_bf16(x.b.z, x.b.w, fx), c);
+// One K-step of 128 bytes, a fragment of each operand: lane l holds the
+// 16-byte pieces l / 16 and 4 + l / 16 of its row.
+__device__ __forceinline__ lf32x4_t mma_bf16_step(const Frag& w, const Frag& x, lf32x4_t c) {
+  c = mma_bf16(__builtin_bit_cast(lbf16x8_t, w.a), __builtin_bit_cast(lbf16x8_t, x.a), c);
+  return mma_bf16(__builtin_bit_cast(lbf16x8_t, w.b), __builtin_bit_cast(lbf16x8_t, x.b), c);
+}
+
+// E4M3 operands on the FP8 matrix instruction, block scales in byte J (I) of
+// sw (sx) for columns 32 (l / 16) .. + 31 (127: none).  The instruction adds 8
+// neighbouring products after cutting each below 2^-13 of the exponent of the
+// largest (measured on the GPU; a sum is then within 2e-5 of its norm), which
+// a bf16 output cannot show; fp32 outputs take mma_decoded.
+template <int J, int I>
+__device__ __forceinline__ lf32x4_t mma_fp8(const Frag& w, const Frag& x, lf32x4_t c, int sw, int sx) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(li32x8_t, w),
+                                                          __builtin_bit_cast(li32x8_t, x), c, 0, 0, J, sw, I, sx);
+}
+
+// E4M3 operands decoded to bf16: every product exact, every sum in fp32 (four
+// bf16 instructions in the place of one).  sw, sx: the rows' four block
+// scales; lane group g's pieces g and 4 + g lie in blocks g / 2 and 2 + g / 2.
+template <bool MX>
+__device__ __forceinline__ lf32x4_t mma_decoded(const Frag& w, const Frag& x, lf32x4_t c, uint32_t sw, uint32_t sx,
+                                                int g) {
+  float w0 = 1.f, w1 = 1.f, x0 = 1.f, x1 = 1.f;
+  if constexpr (MX) {
+    const int sh = 8 * (g >> 1);
+    w0 = e8m0_to_f32((sw >> sh) & 255u);
+    w1 = e8m0_to_f32((sw >> (sh + 16)) & 255u);
+    x0 = e8m0_to_f32((sx >> sh) & 255u);
+    x1 = e8m0_to_f32((sx >> (sh + 16)) & 255u);
   }
+  c = mma_bf16(e4m3_bf16(w.a.x, w.a.y, w0), e4m3_bf16(x.a.x, x.a.y, x0), c);
+  c = mma_bf16(e4m3_bf16(w.a.z, w.a.w, w0), e4m3_bf16(x.a.z, x.a.w, x0), c);
+  c = mma_bf16(e4m3_bf16(w.b.x, w.b.y, w1), e4m3_bf16(x.b.x, x.b.y, x1), c);
+  return mma_bf16(e4m3_bf16(w.b.z, w.b.w, w1), e4m3_bf16(x.b.z, x.b.w, x1), c);
 }
 
 // exp(z) by the hardware exp2 (1 ulp), the rounding of z log2(e) put back:
@@ -89,23 +110,29 @@ __device__ __forceinline__ float act_fn(float z, int fn) {
   }
 }
 
-// One output from its sums (g: the gate's or the only one, u: the up's).
+// One output: what its epilogue reads, then the output from its sums (g: the
+// gate's or the only one, u: the up's).
 template <int QM, bool GATED>
-__device__ __forceinline__ float finish(const LinParams& P, int t, int n, float g, float u) {
-  if constexpr (QM == MOE_Q_FP8) {
-    const float xs = static_cast<const float*>(P.xs)[t];
-    g *= xs * static_cast<const float*>(P.ws)[n];
-    if (GATED) u *= xs * static_cast<const float*>(P.ws)[P.N + n];
+struct Epilogue {
+  float sg = 1.f, su = 1.f, bg = 0.f, bu = 0.f, r = 0.f;
+  __device__ __forceinline__ void load(const LinParams& P, int t, int n) {
+    if constexpr (QM == MOE_Q_FP8) {
+      const float xs = static_cast<const float*>(P.xs)[t];
+      sg = xs * static_cast<const float*>(P.ws)[n];
+      if (GATED) su = xs * static_cast<const float*>(P.ws)[P.N + n];
+    }
+    if (P.bias) {
+      bg = P.bias[n];
+      if (GATED) bu = P.bias[P.N + n];
+    }
+    if (P.res) r = bf16_to_f32(P.res[(int64_t)t * P.ldr + n]);
   }
-  if (P.bias) {
-    g += P.bias[n];
-    if (GATED) u += P.bias[P.N + n];
+  __device__ __forceinline__ float finish(const LinParams& P, float g, float u) const {
+    float y = act_fn(fmaf(g, sg, bg), P.fn);
+    if (GATED) y *= fmaf(u, su, bu);
+    return y + r;
   }
-  float y = act_fn(g, P.fn);
-  if (GATED) y *= u;
-  if (P.res) y += bf16_to_f32(P.res[(int64_t)t * P.ldr + n]);
-  return y;
-}
+};
 
 __device__ __forceinline__ void put(const LinParams& P, int t, int n, float y) {
   if (P.out_f32) static_cast<float*>(P.out)[(int64_t)t * P.ldo + n] = y;
@@ -114,6 +141,9 @@ __device__ __forceinline__ void put(const LinParams& P, int t, int n, float y) {
 
 // The tile kernel (linear_tile.hip).  False: the call's strides do not fit it.
 bool linear_tile_fits(const LinParams& P);
-void launch_linear_tile(const LinParams& P, int qm, hipStream_t s);
+// Its workspace: 0 unless K is split.  kb: bytes of a row; exact: fp32 sums
+// of 8-bit operands (fp32 outputs).
+size_t linear_tile_workspace(int T, int R, int kb, bool exact);
+void launch_linear_tile(const LinParams& P, int qm, void* workspace, hipStream_t s);
 
 }  // namespace moe

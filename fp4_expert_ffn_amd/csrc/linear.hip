@@ -1,6 +1,5 @@
 // The linear product with its epilogue (gfx950): out = fn(x W^T + bias)
-// [* up] + residual, for bf16 operands (v_mfma_f32_16x16x32_bf16) and E4M3
-// operands (decoded to bf16), fp32 accumulation.
+// [* up] + residual, for bf16 and E4M3 operands, fp32 accumulation.
 //
 // Every operand row is read in K-steps of 128 bytes: 128 E4M3 codes or 64
 // bf16 values.
@@ -14,15 +13,20 @@ namespace {
 
 using namespace moe;
 
-// One workgroup: 16 columns (gated: their gate and up rows) x 16 tokens, the
-// K-steps dealt to its 4 waves, their sums joined in LDS in wave order.
-constexpr int kSmallWaves = 4;
+// Few tokens: a stream of the weights.  One workgroup: 16 columns (gated:
+// their gate and up rows) x 16 tokens; its NWV waves take runs of kU K-steps
+// in turn and load a run at once (gated: 16 KiB of weights a wave in flight),
+// so that a row of up to NWV * kU steps costs one memory latency; the waves'
+// sums are joined in LDS in wave order.
+constexpr int kSmallMaxT = 16;  // longer batches: the tile kernel
+constexpr int kU = 4;
 
-template <int QM, bool GATED>
-__global__ __launch_bounds__(64 * kSmallWaves) void k_linear_small(LinParams P, int n_tiles) {
+template <int QM, bool GATED, bool EXACT, int NWV>
+__global__ __launch_bounds__(64 * NWV) void k_linear_small(LinParams P, int n_tiles) {
   constexpr int NB = GATED ? 2 : 1;
-  __shared__ lf32x4_t part[kSmallWaves][NB][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr bool MX = QM == MOE_Q_MXFP8;
+  __shared__ float part[NWV][NB][256];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n0 = (int)(blockIdx.x % n_tiles) * 16, t0 = (int)(blockIdx.x / n_tiles) * 16;
   const int r = lane & 15, g = lane >> 4;
   const int t = min(t0 + r, P.T - 1), n = min(n0 + r, P.N - 1);  // rows past the end re-read the last one
@@ -34,63 +38,108 @@ __global__ __launch_bounds__(64 * kSmallWaves) void k_linear_small(LinParams P, 
 #pragma unroll
   for (int b = 0; b < NB; ++b) acc[b] = lf32x4_t{0.f, 0.f, 0.f, 0.f};
   const int steps = (P.kb + 127) / 128;
-  // Lane l reads bytes 32 (l / 16) .. + 31 of a step: the same permutation of
-  // K in both operands, and for MXFP8 one scale block.  Bytes past the row's
-  // end: a valid piece is loaded and zeroed.
+  // Lane l reads the 16-byte pieces l / 16 and 4 + l / 16 of a step: the FP8
+  // instruction's order of K, of which lane l scales columns 32 (l / 16) .. + 31.
+  // Past the row's end a valid piece is loaded (and zeroed below).
   auto load = [&](const uint8_t* p, int s) {
     Frag f;
-    const int o = s * 128 + g * 32;
-    const uint4 a = *reinterpret_cast<const uint4*>(p + min(o, P.kb - 16));
-    const uint4 b = *reinterpret_cast<const uint4*>(p + min(o + 16, P.kb - 16));
-    const uint32_t ma = o < P.kb ? ~0u : 0u, mb = o + 16 < P.kb ? ~0u : 0u;
-    f.a = make_uint4(a.x & ma, a.y & ma, a.z & ma, a.w & ma);
-    f.b = make_uint4(b.x & mb, b.y & mb, b.z & mb, b.w & mb);
+    const int o = s * 128 + g * 16;
+    f.a = *reinterpret_cast<const uint4*>(p + min(o, P.kb - 16));
+    f.b = *reinterpret_cast<const uint4*>(p + min(o + 64, P.kb - 16));
     return f;
   };
-  for (int s = wave; s < steps; s += kSmallWaves) {
-    const Frag xf = load(xp, s);
-    float fx = 1.f, fw[NB];
+  auto cut = [&](Frag& f, int s) {
+    const int o = s * 128 + g * 16;
+    const uint32_t ma = o < P.kb ? ~0u : 0u, mb = o + 64 < P.kb ? ~0u : 0u;
+    f.a = make_uint4(f.a.x & ma, f.a.y & ma, f.a.z & ma, f.a.w & ma);
+    f.b = make_uint4(f.b.x & mb, f.b.y & mb, f.b.z & mb, f.b.w & mb);
+  };
+  for (int s0 = wave * kU; s0 < steps; s0 += NWV * kU) {
+    Frag fx[kU], fw[kU][NB];
+    uint32_t sx[kU], sw[kU][NB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) fw[b] = 1.f;
-    if constexpr (QM == MOE_Q_MXFP8) {
-      fx = e8m0_to_f32(static_cast<const uint8_t*>(P.xs)[((int64_t)s * P.T + t) * 4 + g]);
+    for (int u = 0; u < kU; ++u) {
+      const int s = min(s0 + u, steps - 1);
+      fx[u] = load(xp, s);
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
-        fw[b] = e8m0_to_f32(static_cast<const uint8_t*>(P.ws)[((int64_t)s * P.R + b * P.N + n) * 4 + g]);
+      for (int b = 0; b < NB; ++b) fw[u][b] = load(wp[b], s);
+      if constexpr (MX) {
+        // the row's four block scales
+        sx[u] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(P.xs) + ((int64_t)s * P.T + t) * 4);
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          sw[u][b] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(P.ws) +
+                                                        ((int64_t)s * P.R + b * P.N + n) * 4);
+      }
     }
 #pragma unroll
-    for (int b = 0; b < NB; ++b) acc[b] = mma_exact<QM>(load(wp[b], s), xf, acc[b], fw[b], fx);
+    for (int u = 0; u < kU; ++u) {
+      if (s0 + u < steps) {
+        if (!MX && s0 + u == steps - 1) {
+          cut(fx[u], s0 + u);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) cut(fw[u][b], s0 + u);
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          if constexpr (QM == MOE_Q_NONE) acc[b] = mma_bf16_step(fw[u][b], fx[u], acc[b]);
+          else if constexpr (EXACT) acc[b] = mma_decoded<MX>(fw[u][b], fx[u], acc[b], MX ? sw[u][b] : 0, MX ? sx[u] : 0, g);
+          else acc[b] = mma_fp8<0, 0>(fw[u][b], fx[u], acc[b], MX ? (int)(sw[u][b] >> (8 * g)) : 127,
+                                      MX ? (int)(sx[u] >> (8 * g)) : 127);
+        }
+      }
+    }
   }
 #pragma unroll
-  for (int b = 0; b < NB; ++b) part[wave][b][lane] = acc[b];
-  __syncthreads();
-  if (wave != 0) return;
+  for (int b = 0; b < NB; ++b) *reinterpret_cast<lf32x4_t*>(&part[wave][b][lane * 4]) = acc[b];
+  // thread o: token o / 16, column o % 16; what its epilogue reads is loaded ahead of the barrier
+  for (int o = tid; o < 256; o += 64 * NWV) {
+    const int to = t0 + o / 16, c = n0 + o % 16;
+    const bool mine = to < P.T && c < P.N;
+    Epilogue<QM, GATED> e;
+    if (mine) e.load(P, to, c);
+    if (o == tid) __syncthreads();
+    if (!mine) continue;
+    const int at = (o / 16 + 16 * ((o % 16) >> 2)) * 4 + (o & 3);
+    float a = 0.f, u = 0.f;
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-#pragma unroll
-    for (int i = 1; i < kSmallWaves; ++i) acc[b] += part[i][b][lane];
+    for (int i = 0; i < NWV; ++i) {
+      a += part[i][0][at];
+      if (GATED) u += part[i][NB - 1][at];
+    }
+    put(P, to, c, e.finish(P, a, u));
   }
-  if (t0 + r >= P.T) return;
-#pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    const int c = n0 + 4 * g + v;
-    if (c < P.N) put(P, t, c, finish<QM, GATED>(P, t, c, acc[0][v], GATED ? acc[NB - 1][v] : 0.f));
-  }
+}
+
+template <int QM, bool GATED, bool EXACT>
+void launch_small_waves(const LinParams& P, hipStream_t s) {
+  const int nt = (P.N + 15) / 16, tt = (P.T + 15) / 16;
+  const dim3 g((unsigned)((long long)nt * tt));
+  const int steps = (P.kb + 127) / 128;
+  if (steps > 8 * kU) launch(k_linear_small<QM, GATED, EXACT, 16>, g, dim3(1024), 0, s, P, nt);
+  else if (steps > 4 * kU) launch(k_linear_small<QM, GATED, EXACT, 8>, g, dim3(512), 0, s, P, nt);
+  else launch(k_linear_small<QM, GATED, EXACT, 4>, g, dim3(256), 0, s, P, nt);
+}
+
+template <int QM, bool GATED>
+void launch_small_gate(const LinParams& P, hipStream_t s) {
+  if (QM != MOE_Q_NONE && P.out_f32) launch_small_waves<QM, GATED, QM != MOE_Q_NONE>(P, s);
+  else launch_small_waves<QM, GATED, false>(P, s);
 }
 
 template <int QM>
 void launch_small(const LinParams& P, hipStream_t s) {
-  const int nt = (P.N + 15) / 16, tt = (P.T + 15) / 16;
-  const dim3 g((unsigned)((long long)nt * tt));
-  if (P.gated) launch(k_linear_small<QM, true>, g, dim3(64 * kSmallWaves), 0, s, P, nt);
-  else launch(k_linear_small<QM, false>, g, dim3(64 * kSmallWaves), 0, s, P, nt);
+  if (P.gated) launch_small_gate<QM, true>(P, s);
+  else launch_small_gate<QM, false>(P, s);
 }
 
 }  // namespace
 
 extern "C" size_t moe_linear_workspace_size(const moe_linear_args* a) {
-  (void)a;
-  return 0;
+  if (!a || a->T <= kSmallMaxT || a->N < 1 || a->K < 1 || a->T >= (1 << 24) || a->N >= (1 << 24) || a->K >= (1 << 24))
+    return 0;
+  const int kb = a->K * (a->qmode == MOE_Q_NONE ? 2 : 1);
+  return linear_tile_workspace(a->T, a->gated ? 2 * a->N : a->N, kb, a->qmode != MOE_Q_NONE && a->out_f32);
 }
 
 extern "C" moe_status moe_linear(const moe_linear_args* a, moe_stream_t stream) {
@@ -137,8 +186,16 @@ extern "C" moe_status moe_linear(const moe_linear_args* a, moe_stream_t stream) 
   P.fn = a->fn;
   P.gated = a->gated;
   P.out_f32 = a->out_f32;
+  const bool tile = a->T > kSmallMaxT && linear_tile_fits(P);
+  const size_t need = tile ? moe_linear_workspace_size(a) : 0;
+  if (need > 0) {
+    if (!a->workspace || a->workspace_bytes < need)
+      return set_error(MOE_ENOMEM, "moe_linear: workspace %zu bytes, needs %zu", a->workspace ? a->workspace_bytes : 0,
+                       need);
+    MOE_CHECK_ARG(!off(a->workspace, 16), "moe_linear: workspace must lie on a 16-byte boundary");
+  }
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (a->T > 32 && linear_tile_fits(P)) launch_linear_tile(P, a->qmode, s);
+  if (tile) launch_linear_tile(P, a->qmode, a->workspace, s);
   else if (a->qmode == MOE_Q_NONE) launch_small<MOE_Q_NONE>(P, s);
   else if (a->qmode == MOE_Q_FP8) launch_small<MOE_Q_FP8>(P, s);
   else launch_small<MOE_Q_MXFP8>(P, s);

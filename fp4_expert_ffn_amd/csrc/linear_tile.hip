@@ -40,12 +40,15 @@ __device__ __forceinline__ void wait_loads() {  // at most N vector-memory opera
 }
 
 struct LinTiles {
-  int mt, nt;      // row and column tiles
+  int mt, nt;            // row and column tiles
   int vec_out, vec_res;  // 16-byte accesses of out and residual rows
+  int splits, per;       // K in `splits` runs of `per` steps
+  float* part;           // splits > 1: the sums [splits][T][R]
 };
 
 // WM x WN waves, each TM x TN 16 x 16 tiles; EXACT: E4M3 operands decoded to
-// bf16 (fp32 outputs).
+// bf16 (fp32 outputs).  With K split, each tile's run of steps leaves its
+// sums in G.part and k_linear_join makes the outputs of them.
 template <int QM, bool GATED, bool EXACT, int WM, int WN, int TM, int TN, int S>
 __global__ __launch_bounds__(64 * WM* WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_linear_tile(LinParams P,
                                                                                                         LinTiles G) {
@@ -74,21 +77,24 @@ __global__ __launch_bounds__(64 * WM* WN) __attribute__((amdgpu_waves_per_eu(2, 
   // Workgroup b runs on XCD b % 8: each XCD takes a contiguous eighth of the
   // tile list, which walks blocks of 4 row tiles column by column, so that
   // the workgroups running at once on an XCD share operand rows in its L2.
-  const int total = G.mt * G.nt, per = (total + 7) / 8;
-  const int L = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
-  if (L >= total) return;
+  // Runs of a split K follow each other, the tiles of one run together.
+  const int tiles = G.mt * G.nt, total = tiles * G.splits, per = (total + 7) / 8;
+  const int LS = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
+  if (LS >= total) return;
+  const int split = LS / tiles, L = LS - split * tiles;
   const int band = L / (4 * G.nt), in_band = L - band * 4 * G.nt;
   const int bh = min(4, G.mt - 4 * band);
   const int t0 = (4 * band + in_band % bh) * BM, n0 = (in_band / bh) * BO;
 
   const uint32_t ring0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)ring;
   const uint32_t mx0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)s_mx;
-  const int steps = (P.kb + 127) / 128;
-  const int tail = MX ? 0 : P.kb & 127;  // bytes of a partial last step, 0: none
+  const int k0 = split * G.per * 128, kb = min(P.kb - k0, G.per * 128);  // this run's bytes of a row
+  const int steps = (kb + 127) / 128;
+  const int tail = MX ? 0 : kb & 127;  // bytes of a partial last step, 0: none
 
   // ---- load addresses: piece (l % 8) ^ (row bits 3:1) of row 8 c + l / 8 of chunk c
-  const uint8_t* abase = P.x + (int64_t)t0 * P.ldx;
-  const uint8_t* bbase = P.w + (int64_t)n0 * P.ldw;
+  const uint8_t* abase = P.x + (int64_t)t0 * P.ldx + k0;
+  const uint8_t* bbase = P.w + (int64_t)n0 * P.ldw + k0;
   uint32_t aoff[CA], boff[CB];
   const int lr = lane >> 3;
   auto piece = [&](int c) { return (lane & 7) ^ ((4 * (c & 1) + (lr >> 1)) & 7); };
@@ -126,6 +132,7 @@ __global__ __launch_bounds__(64 * WM* WN) __attribute__((amdgpu_waves_per_eu(2, 
       sbase = static_cast<const uint8_t*>(P.ws);
       sstep = (int64_t)P.R * 4;
     }
+    sbase += split * (int64_t)G.per * sstep;
   }
   const int64_t up = GATED ? (int64_t)P.N * P.ldw : 0;
   // a partial step's pieces past the row's end re-read its last piece
@@ -197,8 +204,7 @@ __global__ __launch_bounds__(64 * WM* WN) __attribute__((amdgpu_waves_per_eu(2, 
   };
   // The matrix step of fragments j and i.  Block scales: the instruction
   // takes one byte of a register (its number a constant), so the scales of a
-  // half's fragments share one.  EXACT: lane's pieces g and 4 + g lie in
-  // blocks g / 2 and 2 + g / 2 of the step's four.
+  // half's fragments share one.
   static_assert(TH <= 4 && TN <= 4, "scale bytes of a half");
   Frag fw[TN], fx[TM];
   int sw = 0x7F7F7F7F, sx[2] = {0x7F7F7F7F, 0x7F7F7F7F};            // MX
@@ -206,28 +212,10 @@ __global__ __launch_bounds__(64 * WM* WN) __attribute__((amdgpu_waves_per_eu(2, 
   uint32_t ew[MX && EXACT ? TN : 1], ex[MX && EXACT ? TM : 1];     // MX, EXACT: the rows' four scales
   auto mma = [&](auto jc, auto ic) __attribute__((always_inline)) {
     constexpr int j = decltype(jc)::value, i = decltype(ic)::value;
-    const Frag &w = fw[j], &x = fx[i];
     lf32x4_t c = acc[i][j];
-    if constexpr (QM == MOE_Q_NONE) {
-      c = mma_exact<QM>(w, x, c, 1.f, 1.f);
-    } else if constexpr (EXACT) {
-      float w0 = 1.f, w1 = 1.f, x0 = 1.f, x1 = 1.f;
-      if constexpr (MX) {
-        const int sh = 8 * (g >> 1);
-        w0 = e8m0_to_f32((ew[j] >> sh) & 255u);
-        w1 = e8m0_to_f32((ew[j] >> (sh + 16)) & 255u);
-        x0 = e8m0_to_f32((ex[i] >> sh) & 255u);
-        x1 = e8m0_to_f32((ex[i] >> (sh + 16)) & 255u);
-      }
-      c = mma_bf16(e4m3_bf16(w.a.x, w.a.y, w0), e4m3_bf16(x.a.x, x.a.y, x0), c);
-      c = mma_bf16(e4m3_bf16(w.a.z, w.a.w, w0), e4m3_bf16(x.a.z, x.a.w, x0), c);
-      c = mma_bf16(e4m3_bf16(w.b.x, w.b.y, w1), e4m3_bf16(x.b.x, x.b.y, x1), c);
-      c = mma_bf16(e4m3_bf16(w.b.z, w.b.w, w1), e4m3_bf16(x.b.z, x.b.w, x1), c);
-    } else {
-      c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(li32x8_t, w),
-                                                           __builtin_bit_cast(li32x8_t, x), c, 0, 0, j, sw, i % TH,
-                                                           sx[i / TH]);
-    }
+    if constexpr (QM == MOE_Q_NONE) c = mma_bf16_step(fw[j], fx[i], c);
+    else if constexpr (EXACT) c = mma_decoded<MX>(fw[j], fx[i], c, MX ? ew[MX ? j : 0] : 0, MX ? ex[MX ? i : 0] : 0, g);
+    else c = mma_fp8<j, i % TH>(fw[j], fx[i], c, sw, sx[i / TH]);
     acc[i][j] = c;
   };
   // Fragments of the step in work; the halves of fx are read half a step apart.
@@ -376,6 +364,32 @@ __global__ __launch_bounds__(64 * WM* WN) __attribute__((amdgpu_waves_per_eu(2, 
       sx[0] = pack(rx, TH);
     }
   }
+  // (the largest tile never splits: its grids fill the chip)
+  if constexpr (TM * TN <= 16) if (G.splits > 1) {
+    // the sums as they are, 4 columns a lane
+    float* part = G.part + (int64_t)split * P.T * P.R;
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const int q = wn * TN + j;  // 16-row group of the tile
+      const int c = n0 + (GATED ? (q >> 1) * 16 : q * 16) + 4 * g;
+      const int64_t row0 = GATED && (q & 1) ? P.N : 0;
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const int t = t0 + (wm * TM + i) * 16 + r16;
+        if (t >= P.T) continue;
+        float* d = part + (int64_t)t * P.R + row0 + c;
+        if (c + 4 <= P.N && P.N % 4 == 0) {
+          *reinterpret_cast<float4*>(d) = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+        } else {
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            if (c + v < P.N) d[v] = acc[i][j][v];
+        }
+      }
+    }
+    wait_loads<0>();  // no load into LDS outlives the workgroup
+    return;
+  }
   // ---- epilogue.  Lane: token r16 of a 16-token group, weight rows 4 g + v
   // of a group: scales, bias, activation and gate in place; then, through LDS
   // in fp32, rows of 8 columns a lane: the residual and whole 16-byte stores.
@@ -484,14 +498,88 @@ __global__ __launch_bounds__(64 * WM* WN) __attribute__((amdgpu_waves_per_eu(2, 
   }
 }
 
+// The outputs of a split K: the runs' sums added in order, then the
+// epilogue.  One thread a column of a token.
+template <int QM, bool GATED>
+__global__ __launch_bounds__(256) void k_linear_join(LinParams P, const float* __restrict__ part, int splits) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (int64_t)P.T * P.N) return;
+  const int t = (int)(i / P.N), n = (int)(i - (int64_t)t * P.N);
+  const float* p = part + (int64_t)t * P.R + n;
+  const int64_t run = (int64_t)P.T * P.R;
+  float a = 0.f, u = 0.f;
+  Epilogue<QM, GATED> e;
+  e.load(P, t, n);
+  for (int s0 = 0; s0 < splits; s0 += 4) {
+    float v[4], w[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const float* q = p + min(s0 + s, splits - 1) * run;
+      v[s] = q[0];
+      if (GATED) w[s] = q[P.N];
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      if (s0 + s < splits) {
+        a += v[s];
+        if (GATED) u += w[s];
+      }
+    }
+  }
+  put(P, t, n, e.finish(P, a, u));
+}
+
 bool linear_tile_fits(const LinParams& P) {
   // 32-bit offsets inside a tile's rows
   constexpr int64_t lim = 1 << 24;
   return P.ldx < lim && P.ldw < lim && P.ldr < lim && P.ldo < lim;
 }
 
+namespace {
+
+// The tile shapes and what a call of one costs, in us: a step of a tile on a
+// CU, and the rest of a call (launch, first loads, epilogue).  Measured with
+// one or two tiles a CU over 16 to 112 steps (bf16, FP8 and MXFP8 alike: a
+// step is 128 bytes of a row in each).
+struct TileShape {
+  int bm, bn;
+  float step, rest;
+};
+constexpr TileShape kShapes[] = {{256, 256, 1.25f, 10.f}, {128, 256, 0.73f, 6.f}, {128, 128, 0.47f, 5.f},
+                                 {64, 128, 0.32f, 4.5f},  {64, 64, 0.25f, 4.f}};
+constexpr int kCus = 256;
+
+struct TilePlan {
+  int shape, splits, per;
+};
+
+// The shape and the split of K with the least estimated time: tiles in
+// rounds of one a CU; a split costs the join's launch and the sums' way
+// through memory.
+TilePlan plan_tiles(int T, int R, int kb, bool exact) {
+  const int steps = (kb + 127) / 128;
+  TilePlan best{4, 1, steps};
+  float least = 1e30f;
+  for (int i = exact ? 1 : 0; i < 5; ++i) {
+    const TileShape& h = kShapes[i];
+    const int64_t tiles = (int64_t)((T + h.bm - 1) / h.bm) * ((R + h.bn - 1) / h.bn);
+    for (int sp = 1; sp <= (i == 0 ? 1 : 16) && (sp == 1 || steps >= 4 * sp); ++sp) {
+      const int per = (steps + sp - 1) / sp;
+      if ((steps + per - 1) / per != sp) continue;  // an empty run
+      const float rounds = (float)((tiles * sp + kCus - 1) / kCus);
+      const float t = rounds * (per * h.step + (rounds > 1.f ? 0.5f * h.rest : 0.f)) + h.rest +
+                      (sp > 1 ? 3.5f + (float)sp * T * R * 8e-6f / 4.f : 0.f);
+      if (t < least) {
+        least = t;
+        best = TilePlan{i, sp, per};
+      }
+    }
+  }
+  return best;
+}
+
 template <int QM, bool GATED, bool EXACT, int WM, int WN, int TM, int TN, int S>
-static void launch_one(const LinParams& P, hipStream_t s) {
+void launch_one(const LinParams& P, const TilePlan& pl, float* part, hipStream_t s) {
   constexpr int BM = WM * TM * 16, BO = WN * TN * 16 / (GATED ? 2 : 1);
   LinTiles G;
   G.mt = (P.T + BM - 1) / BM;
@@ -499,32 +587,48 @@ static void launch_one(const LinParams& P, hipStream_t s) {
   const int es = P.out_f32 ? 4 : 2;
   G.vec_out = ((uintptr_t)P.out & 15) == 0 && (P.ldo * es) % 16 == 0;
   G.vec_res = ((uintptr_t)P.res & 15) == 0 && P.ldr % 8 == 0;
-  const long long grid = ((long long)G.mt * G.nt + 7) / 8 * 8;
+  G.splits = pl.splits;
+  G.per = pl.per;
+  G.part = part;
+  const long long grid = ((long long)G.mt * G.nt * G.splits + 7) / 8 * 8;
   launch(k_linear_tile<QM, GATED, EXACT, WM, WN, TM, TN, S>, dim3((unsigned)grid), dim3(64 * WM * WN), 0, s, P, G);
+  if (G.splits > 1)
+    launch(k_linear_join<QM, GATED>, dim3((unsigned)(((int64_t)P.T * P.N + 255) / 256)), dim3(256), 0, s, P, part,
+           G.splits);
 }
 
 template <int QM, bool GATED, bool EXACT>
-static void launch_shape(const LinParams& P, hipStream_t s) {
-  const long long big = (long long)((P.T + 255) / 256) * ((P.R + 255) / 256);
+void launch_shape(const LinParams& P, float* part, hipStream_t s) {
+  const TilePlan pl = plan_tiles(P.T, P.R, P.kb, EXACT);
   if constexpr (!EXACT) {
-    if (big >= 192) return launch_one<QM, GATED, EXACT, 2, 4, 8, 4, 2>(P, s);
+    if (pl.shape == 0) return launch_one<QM, GATED, EXACT, 2, 4, 8, 4, 2>(P, pl, part, s);
   }
-  if (big >= 64) launch_one<QM, GATED, EXACT, 2, 4, 4, 4, 3>(P, s);
-  else launch_one<QM, GATED, EXACT, 2, 2, 4, 4, 2>(P, s);
+  if (pl.shape == 1) launch_one<QM, GATED, EXACT, 2, 4, 4, 4, 3>(P, pl, part, s);
+  else if (pl.shape == 2) launch_one<QM, GATED, EXACT, 2, 2, 4, 4, 2>(P, pl, part, s);
+  else if (pl.shape == 3) launch_one<QM, GATED, EXACT, 2, 2, 2, 4, 3>(P, pl, part, s);
+  else launch_one<QM, GATED, EXACT, 2, 1, 2, 4, 3>(P, pl, part, s);
 }
 
 template <int QM, bool EXACT>
-static void launch_gate(const LinParams& P, hipStream_t s) {
-  if (P.gated) launch_shape<QM, true, EXACT>(P, s);
-  else launch_shape<QM, false, EXACT>(P, s);
+void launch_gate(const LinParams& P, float* part, hipStream_t s) {
+  if (P.gated) launch_shape<QM, true, EXACT>(P, part, s);
+  else launch_shape<QM, false, EXACT>(P, part, s);
 }
 
-void launch_linear_tile(const LinParams& P, int qm, hipStream_t s) {
-  if (qm == MOE_Q_NONE) launch_gate<MOE_Q_NONE, false>(P, s);
-  else if (qm == MOE_Q_FP8 && P.out_f32) launch_gate<MOE_Q_FP8, true>(P, s);
-  else if (qm == MOE_Q_FP8) launch_gate<MOE_Q_FP8, false>(P, s);
-  else if (P.out_f32) launch_gate<MOE_Q_MXFP8, true>(P, s);
-  else launch_gate<MOE_Q_MXFP8, false>(P, s);
+}  // namespace
+
+size_t linear_tile_workspace(int T, int R, int kb, bool exact) {
+  const TilePlan pl = plan_tiles(T, R, kb, exact);
+  return pl.splits > 1 ? (size_t)pl.splits * T * R * sizeof(float) : 0;
+}
+
+void launch_linear_tile(const LinParams& P, int qm, void* workspace, hipStream_t s) {
+  float* part = static_cast<float*>(workspace);
+  if (qm == MOE_Q_NONE) launch_gate<MOE_Q_NONE, false>(P, part, s);
+  else if (qm == MOE_Q_FP8 && P.out_f32) launch_gate<MOE_Q_FP8, true>(P, part, s);
+  else if (qm == MOE_Q_FP8) launch_gate<MOE_Q_FP8, false>(P, part, s);
+  else if (P.out_f32) launch_gate<MOE_Q_MXFP8, true>(P, part, s);
+  else launch_gate<MOE_Q_MXFP8, false>(P, part, s);
 }
 
 }  // namespace moe

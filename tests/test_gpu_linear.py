@@ -263,6 +263,20 @@ def test_linear_refuses_bad_strides_and_nulls(m):
     assert m.moe_linear(_ok(m, T=0), stream=0) is None
 
 
+def test_linear_workspace(m):
+    """A call that splits K says so in its workspace size, and refuses a smaller or misaligned one."""
+    assert m.moe_linear_workspace_size(_ok(m, T=1, N=4096, K=8192)) == 0
+    a = _ok(m, T=64, N=64, K=8192)
+    n = m.moe_linear_workspace_size(a)
+    assert n >= 2 * 64 * 64 * 4
+    for p, size, status, msg in ((None, n, 4, "workspace"), (0x40000, n - 1, 4, "workspace"), (0x40008, n, 1, "16-byte")):
+        a.workspace, a.workspace_bytes = p, size
+        with pytest.raises(m.MoeError) as e:
+            m.moe_linear(a, stream=0)
+        assert e.value.status == status and msg in str(e.value)
+    assert m.moe_linear_workspace_size(_ok(m, T=64, N=64, K=8192, out_f32=True, fmt="fp8")) > 0
+
+
 def test_linear_args_refuse_tensors(m):
     x, w = torch.zeros(4, 128, dtype=torch.bfloat16), torch.zeros(32, 128, dtype=torch.bfloat16)
     o = torch.zeros(4, 32, dtype=torch.bfloat16)
