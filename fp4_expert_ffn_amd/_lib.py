@@ -200,7 +200,8 @@ def ptr(t) -> int | None:
 def stream_handle(stream=None) -> int | None:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: the Stream object of torch.cuda.current_stream() costs 2.7 us a call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
