@@ -29,11 +29,11 @@ namespace {
 using namespace moe;
 
 // Threads of a workgroup at most: 1024 (128 registers a lane) while a lane's
-// keys fit them, else 512.  No kernel here spills or
+// keys fit them, else 512 or 256.  No kernel here spills or
 // calls: a register saved where a branch has switched lanes off is lost to
 // them (a CPU test checks the compiled code).
 template <int LR, int NPL>
-constexpr int kMaxThreads = NPL >= 16 ? 512 : 1024;
+constexpr int kMaxThreads = NPL > 16 ? 256 : (NPL == 16 ? 512 : 1024);
 
 constexpr int kChunk = 64;  // tokens of one step of the permutation: a bit each of an expert's 64-bit mask
 
@@ -43,6 +43,7 @@ struct RouterP {
   int sigmoid, n_group, topk_group, top2, renorm;
   int gs;        // experts a group
   int lg, lgs;   // lanes a group (a power of two), its logarithm
+  int vec;       // rows and groups in whole 16-byte pieces
 };
 
 // ------------------------------------------------------------------ 64 bits
@@ -102,6 +103,13 @@ __device__ __forceinline__ double unnorm64(float l, float m) {
 
 __device__ __forceinline__ double unnorm64_key(float l, float m) {
   return l != l ? 0.0 : (l == m ? 1.0 : exp((double)l - (double)m));
+}
+
+// rank_bits without branches.
+__device__ __forceinline__ uint32_t rank32(float v) {
+  const uint32_t u = __float_as_uint(v + 0.f);  // -0 -> +0
+  const uint32_t k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+  return v != v ? 0u : k;
 }
 
 __device__ __forceinline__ float unrank32(uint32_t k) {  // of rank_bits
@@ -256,28 +264,46 @@ __device__ __forceinline__ void choose64(const RouterP& R, const float* lg, int 
 }
 
 // One row by LR lanes (lane p of it): ids[0 .. k) and, in lane j < k, the
-// weight of position j.  lg: E floats of LDS, the row's own, filled here; the
+// weight of position j.  bias_s: the bias in LDS.  lg: E floats of LDS, the row's own, filled here; the
 // wave's rows have theirs side by side, and so have the ids.
 template <int LR, int NPL>
 __device__ __forceinline__ float route_row(const RouterP& R, const float* __restrict__ row, bool valid, int E, int k,
-                                           float* lg, int32_t* ids) {
+                                           const float* bias_s, float* lg, int32_t* ids) {
   constexpr int NPER = LR * NPL / 64 > 16 ? 16 : LR * NPL / 64;  // E <= 1024
   constexpr float kCut = NPL * 0x1p-22f;                        // a word is cut by less than half of this
   const int lane = threadIdx.x & 63, p = lane & (LR - 1);
   const int group = p >> R.lgs, in_group = (p & (R.lg - 1)) * NPL;  // this lane's group and first place in it
   const int base = group * R.gs + in_group;
   const int have = group < R.n_group ? min(max(R.gs - in_group, 0), NPL) : 0;  // experts of this lane
-  float val[NPL];
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) val[i] = i < have && valid ? row[base + i] : 0.f;
-  float bs[NPL];
-  if (R.bias) {
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) bs[i] = i < have ? R.bias[base + i] : 0.f;
+  // the row to LDS in order (a lane's own experts lie too far from its
+  // neighbours' for loads of its own), then each lane's from there
+  if (R.vec) {
+    for (int c = 4 * p; c < E; c += 4 * LR)
+      *reinterpret_cast<float4*>(lg + c) =
+          valid ? *reinterpret_cast<const float4*>(row + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+  } else {
+    for (int c = p; c < E; c += LR) lg[c] = valid ? row[c] : 0.f;
   }
+  __builtin_amdgcn_wave_barrier();  // a wave's LDS accesses keep their order
+  float val[NPL], bs[NPL];
+  if (R.vec) {
 #pragma unroll
-  for (int i = 0; i < NPL; ++i)
-    if (i < have) lg[base + i] = val[i];
+    for (int i = 0; i < NPL; i += 4) {
+      const int at = i < have ? base + i : 0;  // groups are whole pieces: all four or none
+      const float4 v = *reinterpret_cast<const float4*>(lg + at);
+      val[i] = v.x, val[i + 1] = v.y, val[i + 2] = v.z, val[i + 3] = v.w;
+      if (R.bias) {
+        const float4 u = *reinterpret_cast<const float4*>(bias_s + at);
+        bs[i] = u.x, bs[i + 1] = u.y, bs[i + 2] = u.z, bs[i + 3] = u.w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      val[i] = i < have ? lg[base + i] : 0.f;
+      if (R.bias) bs[i] = i < have ? bias_s[base + i] : 0.f;
+    }
+  }
 
   // softmax: largest logit and denominator, in 32 bits for the keys; in 64
   // bits where a weight divides by it
@@ -286,28 +312,31 @@ __device__ __forceinline__ float route_row(const RouterP& R, const float* __rest
   if (!R.sigmoid) {
     uint32_t mk = 0;
 #pragma unroll
-    for (int i = 0; i < NPL; ++i)
-      if (i < have) mk = max(mk, rank_bits(val[i]));
+    for (int i = 0; i < NPL; ++i) mk = max(mk, i < have ? rank32(val[i]) : 0u);
     mk = row_max_u32<LR>(mk);
     m = mk == 0 ? 0.f : unrank32(mk);
     if (R.bias || R.top2) {
       float part = 0.f;
 #pragma unroll
-      for (int i = 0; i < NPL; ++i)
-        if (i < have) part += val[i] != val[i] ? 0.f : (val[i] == m ? 1.f : __expf(val[i] - m));
+      for (int i = 0; i < NPL; ++i) {
+        const float e = val[i] == m ? 1.f : __expf(val[i] - m);
+        part += i < have && val[i] == val[i] ? e : 0.f;
+      }
       inv = 1.0f / row_sum_f32<LR>(part);
     }
     if (!R.renorm) {
       double part64 = 0.0;
 #pragma unroll
-      for (int i = 0; i < NPL; ++i)
-        if (i < have) part64 += unnorm64(val[i], m);
+      for (int i = 0; i < NPL; ++i) {
+        const double d = val[i] == m ? 0.0 : (double)val[i] - (double)m;
+        part64 += i < have && val[i] == val[i] ? exp_neg64(d) : 0.0;
+      }
       den = row_sum_f64<LR>(part64);
     }
   }
   // keys (a NaN logit: NaN), and the two largest of what the groups are ranked by
   float key[NPL], a = -INFINITY, b = -INFINITY;
-  bool unsure = false;
+  bool nan = false;
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
     float sc = val[i];
@@ -315,14 +344,12 @@ __device__ __forceinline__ float route_row(const RouterP& R, const float* __rest
       sc = R.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-val[i]))
                      : (val[i] == m ? inv : __expf(val[i] - m) * inv);
     key[i] = R.bias ? sc + bs[i] : val[i];
-    const float v = R.bias ? key[i] : sc;
-    if (i < have) {
-      unsure = unsure || v != v;
-      b = fmaxf(b, fminf(a, v));
-      a = fmaxf(a, v);
-    }
+    const float v = i < have ? (R.bias ? key[i] : sc) : -INFINITY;
+    nan = nan || v != v;
+    b = fmaxf(b, fminf(a, v));
+    a = fmaxf(a, v);
   }
-  unsure = unsure && R.n_group > 1;  // a NaN is last of its row's keys, but a group's rank is not told by it
+  bool unsure = nan && R.n_group > 1;  // a NaN is last of its row's keys, but a group's rank is not told by it
   // what a comparison of two keys may be off by beside their own rounding: a
   // score's error, below 2^-21 under sigmoid (four roundings of a value below
   // 1) and 2^-19 of the largest under softmax (1 / den, its sum of up to 32
@@ -357,8 +384,10 @@ __device__ __forceinline__ float route_row(const RouterP& R, const float* __rest
   // words: the key's order with its last bits replaced by the place in the lane (the lower place the larger)
   uint32_t w[NPL];
 #pragma unroll
-  for (int i = 0; i < NPL; ++i)
-    w[i] = i < have && live ? (rank_bits(key[i]) & ~(uint32_t)(NPL - 1)) | (uint32_t)(NPL - 1 - i) : 0u;
+  for (int i = 0; i < NPL; ++i) {
+    const uint32_t k1 = (rank32(key[i]) & ~(uint32_t)(NPL - 1)) | (uint32_t)(NPL - 1 - i);
+    w[i] = i < have && live ? k1 : 0u;
+  }
   sort_desc<NPL>(w);
   float last = 0.f;
   int took = 0;
@@ -371,9 +400,11 @@ __device__ __forceinline__ float route_row(const RouterP& R, const float* __rest
     const bool hit = w[0] == mx;  // more lanes than one: equal words, counted below
     if (hit) ids[r] = base + NPL - 1 - (int)(mx & (NPL - 1));
     took += hit;
+    // by bits (v_bfi): of selects between neighbours the compiler makes an indexed array, 430 instructions a round
+    const uint32_t up = hit ? ~0u : 0u;
 #pragma unroll
-    for (int i = 0; i + 1 < NPL; ++i) w[i] = hit ? w[i + 1] : w[i];
-    w[NPL - 1] = hit ? 0u : w[NPL - 1];
+    for (int i = 0; i + 1 < NPL; ++i) w[i] = (w[i + 1] & up) | (w[i] & ~up);
+    w[NPL - 1] &= ~up;
   }
   const float all = row_sum_f32<LR>((float)took);  // by every lane of the row, also where unsure is set already
   unsure = unsure || all != (float)k;
@@ -405,7 +436,7 @@ __device__ __forceinline__ float route_row(const RouterP& R, const float* __rest
 }
 
 // `rows` rows from token t0 on by the workgroup: ids to LDS (ids_s [64][k])
-// and memory, weights to memory.  lg_s: E floats for each row in work.
+// and memory, weights to memory.  lg_s: E floats of the bias, then E for each row in work.
 template <int LR, int NPL>
 __device__ __forceinline__ void route_rows(const RouterP& R, const float* __restrict__ logits, int t0, int rows, int E,
                                            int k, float* lg_s, int32_t* ids_s, int32_t* __restrict__ ids,
@@ -413,12 +444,16 @@ __device__ __forceinline__ void route_rows(const RouterP& R, const float* __rest
   constexpr int RPW = 64 / LR;  // rows a wave
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, rpp = (int)(blockDim.x >> 6) * RPW;
   const int slot = wave * RPW + lane / LR, p = lane & (LR - 1);
+  if (R.bias) {
+    for (int e = threadIdx.x; e < E; e += blockDim.x) lg_s[e] = R.bias[e];
+    __syncthreads();
+  }
   for (int r0 = 0; r0 < rows; r0 += rpp) {
     const int r = r0 + slot;
     if (r0 + wave * RPW >= rows) break;  // whole waves
     const bool valid = r < rows;
-    const float w = route_row<LR, NPL>(R, logits + (size_t)(t0 + (valid ? r : 0)) * E, valid, E, k, lg_s + slot * E,
-                                       ids_s + r * k);
+    const float w = route_row<LR, NPL>(R, logits + (size_t)(t0 + (valid ? r : 0)) * E, valid, E, k, lg_s,
+                                       lg_s + (slot + 1) * E, ids_s + r * k);
     if (p < k && valid) {
       ids[(size_t)(t0 + r) * k + p] = ids_s[r * k + p];
       wts[(size_t)(t0 + r) * k + p] = w;
@@ -429,7 +464,7 @@ __device__ __forceinline__ void route_rows(const RouterP& R, const float* __rest
 template <int LR, int NPL>
 __global__ __launch_bounds__(256) void k_route_scored(RouterP R, const float* __restrict__ logits, int T, int E, int k,
                                                       int32_t* __restrict__ ids, float* __restrict__ wts) {
-  extern __shared__ float lg_s[];
+  extern __shared__ __align__(16) float lg_s[];
   constexpr int ROWS = 4 * (64 / LR);
   __shared__ int32_t ids_s[ROWS * kRouteMaxK];
   const int t0 = (int)blockIdx.x * ROWS;
@@ -499,7 +534,7 @@ __global__ __launch_bounds__((kMaxThreads<LR, NPL>)) void k_route_one(RouterP R,
                                                     int32_t* __restrict__ ids, float* __restrict__ wts,
                                                     int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
                                                     int32_t* __restrict__ perm, int32_t* __restrict__ inv) {
-  extern __shared__ uint64_t tmask[];
+  extern __shared__ __align__(16) uint64_t tmask[];
   __shared__ int32_t ids_s[kChunk * kRouteMaxK], wsum[16];
   int32_t* off = reinterpret_cast<int32_t*>(tmask + E);
   float* lg_s = reinterpret_cast<float*>(off + E);
@@ -526,7 +561,7 @@ template <int LR, int NPL>
 __global__ __launch_bounds__((kMaxThreads<LR, NPL>)) void k_route_chunk(RouterP R, const float* __restrict__ logits, int T, int E, int k,
                                                       int32_t* __restrict__ ids, float* __restrict__ wts,
                                                       int32_t* __restrict__ inv) {
-  extern __shared__ int32_t cnt[];  // [E], then the rows' logits
+  extern __shared__ __align__(16) int32_t cnt[];  // [E], then the rows' logits
   __shared__ int32_t ids_s[kChunk * kRouteMaxK];
   const int t0 = (int)blockIdx.x * kChunk, rows = min(kChunk, T - t0);
   for (int e = threadIdx.x; e < E; e += blockDim.x) cnt[e] = 0;
@@ -653,7 +688,7 @@ void with_shape(RouterP& R, int E, bool one, F f) {
   }
 }
 
-RouterP router_params(const moe_router* r, int E) {
+RouterP router_params(const moe_router* r, const float* logits, int E) {
   RouterP R{};
   R.bias = r->bias;
   R.scale = r->scale;
@@ -663,6 +698,7 @@ RouterP router_params(const moe_router* r, int E) {
   R.top2 = r->n_group > 1 && r->group_rank == MOE_GROUP_TOP2;
   R.renorm = r->renormalize;
   R.gs = E / r->n_group;
+  R.vec = E % 4 == 0 && R.gs % 4 == 0 && ((uintptr_t)logits & 15) == 0;
   return R;
 }
 
@@ -682,11 +718,11 @@ extern "C" moe_status moe_route_scored(const moe_router* r, const float* logits,
   if (st != MOE_OK) return st;
   if (T == 0) return MOE_OK;
   MOE_CHECK_ARG(logits && topk_ids && topk_w, "moe_route_scored: null pointer");
-  RouterP R = router_params(r, E);
+  RouterP R = router_params(r, logits, E);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   with_shape(R, E, T <= 64, [&](auto lr, auto npl) {
     constexpr int LR = decltype(lr)::value, NPL = decltype(npl)::value, ROWS = 4 * (64 / LR);
-    const size_t lds = (size_t)ROWS * E * sizeof(float);  // at most 16 KiB
+    const size_t lds = (size_t)(ROWS + 1) * E * sizeof(float);  // at most 20 KiB
     launch(k_route_scored<LR, NPL>, dim3((unsigned)((T + ROWS - 1) / ROWS)), dim3(256), lds, s, R, logits, T, E, k,
            topk_ids, topk_w);
   });
@@ -708,7 +744,7 @@ extern "C" moe_status moe_route_scored_permute(const moe_router* r, const float*
     if (st != MOE_OK) return st;
     return moe_permute(topk_ids, T, k, E, counts, offsets, perm, inv, stream);
   }
-  RouterP R = router_params(r, E);
+  RouterP R = router_params(r, logits, E);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   hipError_t err = hipSuccess;
   if (T <= kChunk) {
@@ -717,7 +753,7 @@ extern "C" moe_status moe_route_scored_permute(const moe_router* r, const float*
       const int waves = std::min(kMaxThreads<LR, NPL> / 64, (T + RPW - 1) / RPW);
       // (at least) four waves for the scan over the experts
       const int nw = std::max(waves, std::min(4, (E + 63) / 64));
-      const size_t lds = (size_t)E * 12 + (size_t)nw * RPW * E * sizeof(float);
+      const size_t lds = (size_t)E * 12 + (size_t)(nw * RPW + 1) * E * sizeof(float);
       err = allow_lds(k_route_one<LR, NPL>, lds);
       if (err != hipSuccess) return;
       launch(k_route_one<LR, NPL>, dim3(1), dim3((unsigned)(64 * nw)), lds, s, R, logits, T, E, k, topk_ids, topk_w,
@@ -728,7 +764,7 @@ extern "C" moe_status moe_route_scored_permute(const moe_router* r, const float*
     with_shape(R, E, false, [&](auto lr, auto npl) {
       constexpr int LR = decltype(lr)::value, NPL = decltype(npl)::value;
       constexpr int NT = kMaxThreads<LR, NPL>;
-      const size_t lds = (size_t)E * 4 + (size_t)(NT / LR) * E * sizeof(float);
+      const size_t lds = (size_t)E * 4 + (size_t)(NT / LR + 1) * E * sizeof(float);
       err = allow_lds(k_route_chunk<LR, NPL>, lds);
       if (err != hipSuccess) return;
       launch(k_route_chunk<LR, NPL>, dim3(chunks), dim3(NT), lds, s, R, logits, T, E, k, topk_ids, topk_w, inv);
