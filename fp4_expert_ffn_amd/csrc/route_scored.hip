@@ -8,8 +8,10 @@
 // The choice has to be the rule's in 64 bits, but 64-bit keys of every expert
 // would be most of the work.  So a row is chosen by 32-bit keys first, and
 // every comparison that decided something is checked against a bound of its
-// error; a row with one that could have gone the other way (ties among them)
-// is chosen again by one wave with 64-bit keys.
+// error.  Groups whose place is open are ranked again in 64 bits, and so are
+// the last places taken and their neighbours; a row that more than 16
+// candidates are open for, or that holds equal words, is chosen again whole
+// by one wave with 64-bit keys.
 //
 // Fast choice: LR lanes a row (64 / LR rows a wave), NPL consecutive experts a
 // lane.  A lane sorts its keys once (a Batcher network on 32-bit words that
@@ -33,9 +35,9 @@ using namespace moe;
 // calls: a register saved where a branch has switched lanes off is lost to
 // them (a CPU test checks the compiled code).
 template <int LR, int NPL>
-constexpr int kMaxThreads = NPL > 16 ? 256 : (NPL == 16 ? 512 : 1024);
+constexpr int kMaxThreads = NPL > 16 ? 256 : (NPL >= 8 ? 512 : 1024);
 
-constexpr int kChunk = 64;  // tokens of one step of the permutation: a bit each of an expert's 64-bit mask
+constexpr int kChunk = 64;  // tokens of a chunk of the permutation at most: a bit each of an expert's 64-bit mask
 
 struct RouterP {
   const float* bias;
@@ -153,6 +155,15 @@ __device__ __forceinline__ double row_sum_f64(double v) {
   return v;
 }
 
+// The softmax denominator of a row for its keys, from the lanes' parts of it in LDS.
+template <int LR>
+__device__ __forceinline__ double softmax_den64(const float* lg, int base, int have, float m) {
+  double part = 0.0;
+#pragma unroll 1
+  for (int i = 0; i < have; ++i) part += unnorm64_key(lg[base + i], m);
+  return row_sum_f64<LR>(part);
+}
+
 // A group's two largest, from two disjoint parts of it.
 __device__ __forceinline__ void merge2(float& a, float& b, float a2, float b2) {
   const float lo = fminf(a, a2);
@@ -263,9 +274,9 @@ __device__ __forceinline__ void choose64(const RouterP& R, const float* lg, int 
   }
 }
 
-// One row by LR lanes (lane p of it): ids[0 .. k) and, in lane j < k, the
+// One row by LR >= 16 lanes (lane p of it): ids[0 .. k) and, in lane j < k, the
 // weight of position j.  bias_s: the bias in LDS.  lg: E floats of LDS, the row's own, filled here; the
-// wave's rows have theirs side by side, and so have the ids.
+// wave's rows have theirs side by side, and so have the ids (kRouteMaxK words a row).
 template <int LR, int NPL>
 __device__ __forceinline__ float route_row(const RouterP& R, const float* __restrict__ row, bool valid, int E, int k,
                                            const float* bias_s, float* lg, int32_t* ids) {
@@ -326,10 +337,11 @@ __device__ __forceinline__ float route_row(const RouterP& R, const float* __rest
     }
     if (!R.renorm) {
       double part64 = 0.0;
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) {
-        const double d = val[i] == m ? 0.0 : (double)val[i] - (double)m;
-        part64 += i < have && val[i] == val[i] ? exp_neg64(d) : 0.0;
+#pragma unroll 2
+      for (int i = 0; i < NPL; ++i) {  // from LDS again: unrolled whole, its temporaries would cost a wave's place
+        const float l = i < have ? lg[base + i] : NAN;
+        const double d = l == m ? 0.0 : (double)l - (double)m;
+        part64 += l == l ? exp_neg64(d) : 0.0;
       }
       den = row_sum_f64<LR>(part64);
     }
@@ -349,7 +361,6 @@ __device__ __forceinline__ float route_row(const RouterP& R, const float* __rest
     b = fmaxf(b, fminf(a, v));
     a = fmaxf(a, v);
   }
-  bool unsure = nan && R.n_group > 1;  // a NaN is last of its row's keys, but a group's rank is not told by it
   // what a comparison of two keys may be off by beside their own rounding: a
   // score's error, below 2^-21 under sigmoid (four roundings of a value below
   // 1) and 2^-19 of the largest under softmax (1 / den, its sum of up to 32
@@ -368,17 +379,57 @@ __device__ __forceinline__ float route_row(const RouterP& R, const float* __rest
     // (exp of a difference of up to 88).
     const bool exact = !R.top2 && !R.bias;
     const float tol = 2.f * s_err + (R.bias ? 0x1p-19f : 0x1p-16f) * fabsf(rank) + 0x1p-100f;
-    int place = 0;
+    int above = 0, maybe = 0;  // groups surely before this one, and possibly
     const int lanes = R.n_group << R.lgs, first = lane - p;
     for (int d = 1; d < R.n_group; ++d) {
       int q = p + (d << R.lgs);
       q = q >= lanes ? q - lanes : q;
       const float other = __shfl(rank, first + (q & (LR - 1)));
-      place += other > rank || (other == rank && q < p);
-      unsure = unsure || !(exact || fabsf(other - rank) > tol);
+      const bool before = other > rank || (other == rank && q < p);
+      above += exact ? before : other - rank > tol;
+      maybe += exact ? before : !(rank - other > tol);
     }
-    live = live && place < R.topk_group;
-    unsure = unsure && group < R.n_group;
+    live = live && maybe < R.topk_group;
+    // rows whose groups are open (a NaN among the keys leaves the ranks above
+    // without meaning): their groups in 64 bits
+    const uint64_t open = __ballot(group < R.n_group && (nan || (maybe >= R.topk_group && above < R.topk_group)));
+    if (open != 0ull) {
+      const uint64_t row_mask = (LR == 64 ? ~0ull : (1ull << (LR & 63)) - 1ull) << (lane - p);
+      double den64 = 1.0;
+      if (!R.sigmoid && !exact) den64 = softmax_den64<LR>(lg, base, have, m);
+      double a64 = -INFINITY, b64 = -INFINITY;
+      int real = 0;
+#pragma unroll 1
+      for (int i = 0; i < have; ++i) {
+        const float l = lg[base + i];
+        double v = (double)l;
+        if (!exact) {
+          v = l != l ? v : (R.sigmoid ? sigmoid64((double)l) : unnorm64_key(l, m) / den64);
+          if (R.bias) v += (double)bias_s[base + i];
+        }
+        real |= v == v;
+        v = v != v ? -INFINITY : v;
+        b64 = fmax(b64, fmin(a64, v));
+        a64 = fmax(a64, v);
+      }
+      for (int o = 1; o < R.lg; o <<= 1) {
+        const double a2 = __shfl_xor(a64, o), b2 = __shfl_xor(b64, o);
+        real |= __shfl_xor(real, o);
+        b64 = fmax(fmin(a64, a2), fmax(b64, b2));
+        a64 = fmax(a64, a2);
+      }
+      const uint64_t mine = R.top2 && R.gs > 1 ? rank64(a64 + b64) : (real ? rank64(a64) : 1ull);
+      int place = 0;
+      for (int d = 1; d < R.n_group; ++d) {
+        int q = p + (d << R.lgs);
+        q = q >= lanes ? q - lanes : q;
+        const int src = first + (q & (LR - 1));
+        const uint64_t other =
+            ((uint64_t)(uint32_t)__shfl((int)(mine >> 32), src) << 32) | (uint32_t)__shfl((int)(uint32_t)mine, src);
+        place += other > mine || (other == mine && q < p);
+      }
+      if (open & row_mask) live = group < R.n_group && place < R.topk_group;
+    }
   }
 
   // words: the key's order with its last bits replaced by the place in the lane (the lower place the larger)
@@ -389,25 +440,53 @@ __device__ __forceinline__ float route_row(const RouterP& R, const float* __rest
     w[i] = i < have && live ? k1 : 0u;
   }
   sort_desc<NPL>(w);
+  // Candidates in the words' order: the first k, and after them while one
+  // could still belong before the last (lanes 0 .. 15 hold one each below).
   float last = 0.f;
-  int took = 0;
-  for (int r = 0; r <= k; ++r) {  // round k: only what follows the last one taken
+  int took = 0, n = kRouteMaxK + 1;  // n: the row's candidates, once its end is certain
+  bool near = false;
+  for (int r = 0; r <= kRouteMaxK; ++r) {
     const uint32_t mx = row_max_u32<LR>(w[0]);
     const float v = unrank32(mx & ~(uint32_t)(NPL - 1));
-    if (r > 0 && (r < k || mx != 0u)) unsure = unsure || !(last - v > s_err + kCut * fmaxf(fabsf(last), fabsf(v)));
-    if (r == k) break;
+    const bool close = r > 0 && !(last - v > s_err + kCut * fmaxf(fabsf(last), fabsf(v)));
+    if (r >= k && (mx == 0u || !close)) n = min(n, r);
+    if (r >= k && __ballot(n > r) == 0ull) break;  // every row of the wave ends here
+    if (r == kRouteMaxK) break;
+    near = near || (close && r < n);
     last = v;
     const bool hit = w[0] == mx;  // more lanes than one: equal words, counted below
-    if (hit) ids[r] = base + NPL - 1 - (int)(mx & (NPL - 1));
-    took += hit;
+    if (hit && r < n) ids[r] = base + NPL - 1 - (int)(mx & (NPL - 1));
+    took += hit && r < n;
     // by bits (v_bfi): of selects between neighbours the compiler makes an indexed array, 430 instructions a round
     const uint32_t up = hit ? ~0u : 0u;
 #pragma unroll
     for (int i = 0; i + 1 < NPL; ++i) w[i] = (w[i + 1] & up) | (w[i] & ~up);
     w[NPL - 1] &= ~up;
   }
-  const float all = row_sum_f32<LR>((float)took);  // by every lane of the row, also where unsure is set already
-  unsure = unsure || all != (float)k;
+  const bool unsure = row_sum_f32<LR>((float)took) != (float)n || n > kRouteMaxK;
+  near = near && !unsure;
+  // rows whose order is open among their candidates alone: those in 64 bits
+  if (__ballot(near && valid) != 0ull) {
+    double den64 = 1.0;
+    if (R.bias && !R.sigmoid) den64 = softmax_den64<LR>(lg, base, have, m);
+    const int id = p < n && p < kRouteMaxK && near ? ids[p] : 0;
+    uint64_t mine = 0;
+    if (p < n && p < kRouteMaxK && near) {
+      const float l = lg[id];
+      double key64 = (double)l;
+      if (R.bias)
+        key64 = (l != l ? key64 : (R.sigmoid ? sigmoid64((double)l) : unnorm64_key(l, m) / den64)) + (double)bias_s[id];
+      mine = rank64(key64);
+    }
+    int place = 0;
+    for (int q = 0; q < kRouteMaxK; ++q) {
+      const uint64_t other = ((uint64_t)(uint32_t)__shfl((int)(mine >> 32), lane - p + q) << 32) |
+                             (uint32_t)__shfl((int)(uint32_t)mine, lane - p + q);
+      const int oid = __shfl(id, lane - p + q);
+      place += other > mine || (other == mine && oid < id);
+    }
+    if (mine != 0 && place < k) ids[place] = id;
+  }
   // rows whose choice could differ in 64 bits: again, one wave each
   uint64_t again = __ballot(unsure && valid);
   while (again) {
@@ -416,7 +495,7 @@ __device__ __forceinline__ float route_row(const RouterP& R, const float* __rest
     const float mr = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(m), l0));
     const int seg = l0 / LR;
     const float* lrow = lg + (seg - (lane / LR)) * E;
-    int32_t* irow = ids + (seg - (lane / LR)) * k;
+    int32_t* irow = ids + (seg - (lane / LR)) * kRouteMaxK;
     double dr = 1.0;
     if (!R.sigmoid && (R.bias || R.top2)) {
       double part = 0.0;
@@ -435,7 +514,7 @@ __device__ __forceinline__ float route_row(const RouterP& R, const float* __rest
   return (float)((den > 0.0 ? s / den : 1.0 / k) * (double)R.scale);
 }
 
-// `rows` rows from token t0 on by the workgroup: ids to LDS (ids_s [64][k])
+// `rows` rows from token t0 on by the workgroup: ids to LDS (ids_s [64][kRouteMaxK])
 // and memory, weights to memory.  lg_s: E floats of the bias, then E for each row in work.
 template <int LR, int NPL>
 __device__ __forceinline__ void route_rows(const RouterP& R, const float* __restrict__ logits, int t0, int rows, int E,
@@ -453,9 +532,9 @@ __device__ __forceinline__ void route_rows(const RouterP& R, const float* __rest
     if (r0 + wave * RPW >= rows) break;  // whole waves
     const bool valid = r < rows;
     const float w = route_row<LR, NPL>(R, logits + (size_t)(t0 + (valid ? r : 0)) * E, valid, E, k, lg_s,
-                                       lg_s + (slot + 1) * E, ids_s + r * k);
+                                       lg_s + (slot + 1) * E, ids_s + r * kRouteMaxK);
     if (p < k && valid) {
-      ids[(size_t)(t0 + r) * k + p] = ids_s[r * k + p];
+      ids[(size_t)(t0 + r) * k + p] = ids_s[r * kRouteMaxK + p];
       wts[(size_t)(t0 + r) * k + p] = w;
     }
   }
@@ -473,15 +552,17 @@ __global__ __launch_bounds__(256) void k_route_scored(RouterP R, const float* __
 
 // ------------------------------------------------------------------ permutation
 //
-// In chunks of 64 tokens.  A token takes an expert at most once, so an expert's
-// rows of a chunk are the set bits of a 64-bit mask of the chunk's tokens, and
+// In chunks of 16, 32 or 64 tokens.  A token takes an expert at most once, so
+// an expert's rows of a chunk are the set bits of a 64-bit mask of its tokens, and
 // the position of (t, e) is offsets[e] + (rows of e in earlier chunks) + (set
 // bits below t): no sort and no order-dependent atomics.
 
-// tmask[e] of a chunk (cleared before) from its ids.
+// tmask[e] of a chunk (cleared before) from its ids (LDS, kRouteMaxK words a token).
 __device__ __forceinline__ void set_masks(const int32_t* ids, int n, int k, uint64_t* tmask) {
-  for (int f = threadIdx.x; f < n; f += blockDim.x)
-    atomicOr(reinterpret_cast<unsigned long long*>(&tmask[ids[f]]), 1ull << (f / k));
+  for (int f = threadIdx.x; f < n; f += blockDim.x) {
+    const int t = f / k;
+    atomicOr(reinterpret_cast<unsigned long long*>(&tmask[ids[t * kRouteMaxK + f - t * k]]), 1ull << t);
+  }
 }
 
 // Exclusive scan over the experts of cnt(e) by the workgroup; calls
@@ -521,8 +602,8 @@ __device__ __forceinline__ int scan_experts(int E, int32_t* wsum, C cnt, O out) 
 __device__ __forceinline__ void place(const int32_t* ids, int f0, int n, int k, const uint64_t* tmask,
                                       const int32_t* off, int32_t* __restrict__ perm, int32_t* __restrict__ inv) {
   for (int f = threadIdx.x; f < n; f += blockDim.x) {
-    const int e = ids[f];
-    const int pos = off[e] + (int)__popcll(tmask[e] & ((1ull << (f / k)) - 1ull));
+    const int t = f / k, e = ids[t * kRouteMaxK + f - t * k];
+    const int pos = off[e] + (int)__popcll(tmask[e] & ((1ull << t) - 1ull));
     perm[pos] = f0 + f;
     inv[f0 + f] = pos;
   }
@@ -555,35 +636,39 @@ __global__ __launch_bounds__((kMaxThreads<LR, NPL>)) void k_route_one(RouterP R,
   place(ids_s, 0, T * k, k, tmask, off, perm, inv);
 }
 
-// Longer batches, first pass: a chunk's rows, and the counts of a whole chunk
-// to the chunk's own part of inv (E <= 64 k words; the last pass replaces it).
+// Longer batches, first pass: a chunk's rows (C tokens), and the counts of a
+// whole chunk to the chunk's own part of inv (E <= C k words; the last pass
+// replaces it).
 template <int LR, int NPL>
-__global__ __launch_bounds__((kMaxThreads<LR, NPL>)) void k_route_chunk(RouterP R, const float* __restrict__ logits, int T, int E, int k,
-                                                      int32_t* __restrict__ ids, float* __restrict__ wts,
-                                                      int32_t* __restrict__ inv) {
-  extern __shared__ __align__(16) int32_t cnt[];  // [E], then the rows' logits
+__global__ __launch_bounds__((kMaxThreads<LR, NPL>)) void k_route_chunk(RouterP R, const float* __restrict__ logits,
+                                                                       int T, int E, int k, int C,
+                                                                       int32_t* __restrict__ ids,
+                                                                       float* __restrict__ wts,
+                                                                       int32_t* __restrict__ inv) {
+  extern __shared__ __align__(16) int32_t cnt[];  // [E], then the bias and the rows' logits
   __shared__ int32_t ids_s[kChunk * kRouteMaxK];
-  const int t0 = (int)blockIdx.x * kChunk, rows = min(kChunk, T - t0);
+  const int t0 = (int)blockIdx.x * C, rows = min(C, T - t0);
   for (int e = threadIdx.x; e < E; e += blockDim.x) cnt[e] = 0;
   route_rows<LR, NPL>(R, logits, t0, rows, E, k, reinterpret_cast<float*>(cnt + E), ids_s, ids, wts);
-  if (rows < kChunk) return;
+  if (rows < C) return;
   __syncthreads();
-  for (int f = threadIdx.x; f < rows * k; f += blockDim.x) atomicAdd(&cnt[ids_s[f]], 1);
+  for (int f = threadIdx.x; f < rows * k; f += blockDim.x)
+    atomicAdd(&cnt[ids_s[f / k * kRouteMaxK + f % k]], 1);
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += blockDim.x) inv[(size_t)t0 * k + e] = cnt[e];
 }
 
 // Second pass, a workgroup an expert: the chunks' counts become the rows of
 // the earlier chunks; counts[e] their sum, with the last, partial chunk's.
-__global__ __launch_bounds__(256) void k_chunk_scan(const int32_t* __restrict__ ids, int T, int k,
+__global__ __launch_bounds__(256) void k_chunk_scan(const int32_t* __restrict__ ids, int T, int k, int C,
                                                     int32_t* __restrict__ inv, int32_t* __restrict__ counts) {
   __shared__ int32_t wsum[4];
   const int e = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int whole = T / kChunk;
+  const int whole = T / C;
   int run = 0;
   for (int c0 = 0; c0 < whole; c0 += 256) {
     const int c = c0 + tid;
-    int32_t* at = inv + (size_t)c * kChunk * k + e;
+    int32_t* at = inv + (size_t)c * C * k + e;
     const int n = c < whole ? *at : 0;
     int incl = n;
 #pragma unroll
@@ -602,7 +687,7 @@ __global__ __launch_bounds__(256) void k_chunk_scan(const int32_t* __restrict__ 
     __syncthreads();
   }
   int mine = 0;  // the partial chunk's rows
-  for (int f = whole * kChunk * k + tid; f < T * k; f += 256) mine += ids[f] == e;
+  for (int f = whole * C * k + tid; f < T * k; f += 256) mine += ids[f] == e;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) mine += __shfl_xor(mine, o);
   if (lane == 0) wsum[wave] = mine;
@@ -611,15 +696,15 @@ __global__ __launch_bounds__(256) void k_chunk_scan(const int32_t* __restrict__ 
 }
 
 // Third pass, a workgroup a chunk.  LDS: E masks, E offsets.
-__global__ __launch_bounds__(512) void k_chunk_place(const int32_t* __restrict__ ids, int T, int E, int k,
+__global__ __launch_bounds__(512) void k_chunk_place(const int32_t* __restrict__ ids, int T, int E, int k, int C,
                                                      const int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
                                                      int32_t* __restrict__ perm, int32_t* __restrict__ inv) {
   extern __shared__ uint64_t tmask[];
   __shared__ int32_t wsum[8], ids_s[kChunk * kRouteMaxK];
   int32_t* off = reinterpret_cast<int32_t*>(tmask + E);
-  const int t0 = (int)blockIdx.x * kChunk, rows = min(kChunk, T - t0), n = rows * k, f0 = t0 * k;
+  const int t0 = (int)blockIdx.x * C, rows = min(C, T - t0), n = rows * k, f0 = t0 * k;
   for (int e = threadIdx.x; e < E; e += blockDim.x) tmask[e] = 0ull;
-  for (int f = threadIdx.x; f < n; f += blockDim.x) ids_s[f] = ids[f0 + f];
+  for (int f = threadIdx.x; f < n; f += blockDim.x) ids_s[f / k * kRouteMaxK + f % k] = ids[f0 + f];
   __syncthreads();
   set_masks(ids_s, n, k, tmask);
   __syncthreads();
@@ -627,7 +712,7 @@ __global__ __launch_bounds__(512) void k_chunk_place(const int32_t* __restrict__
       E, wsum, [&](int e) { return counts[e]; },
       [&](int e, int base, int c) {
         // a partial chunk is the last one: its rows end the expert's
-        off[e] = base + (rows == kChunk ? inv[(size_t)f0 + e] : c - (int)__popcll(tmask[e]));
+        off[e] = base + (rows == C ? inv[(size_t)f0 + e] : c - (int)__popcll(tmask[e]));
         if (blockIdx.x == 0) offsets[e] = base;
       });
   if (blockIdx.x == 0 && threadIdx.x == 0) offsets[E] = T * k;
@@ -760,18 +845,22 @@ extern "C" moe_status moe_route_scored_permute(const moe_router* r, const float*
              counts, offsets, perm, inv);
     });
   } else {
-    const unsigned chunks = (unsigned)((T + kChunk - 1) / kChunk);
+    // the smallest chunk whose part of inv holds its counts: the most workgroups
+    const int C = E <= 16 * k ? 16 : (E <= 32 * k ? 32 : kChunk);
+    const unsigned chunks = (unsigned)((T + C - 1) / C);
     with_shape(R, E, false, [&](auto lr, auto npl) {
       constexpr int LR = decltype(lr)::value, NPL = decltype(npl)::value;
-      constexpr int NT = kMaxThreads<LR, NPL>;
-      const size_t lds = (size_t)E * 4 + (size_t)(NT / LR + 1) * E * sizeof(float);
+      const int nt = std::min(kMaxThreads<LR, NPL>, C * LR);
+      const size_t lds = (size_t)E * 4 + (size_t)(nt / LR + 1) * E * sizeof(float);
       err = allow_lds(k_route_chunk<LR, NPL>, lds);
       if (err != hipSuccess) return;
-      launch(k_route_chunk<LR, NPL>, dim3(chunks), dim3(NT), lds, s, R, logits, T, E, k, topk_ids, topk_w, inv);
+      launch(k_route_chunk<LR, NPL>, dim3(chunks), dim3((unsigned)nt), lds, s, R, logits, T, E, k, C, topk_ids, topk_w,
+             inv);
     });
     if (err == hipSuccess) {
-      launch(k_chunk_scan, dim3((unsigned)E), dim3(256), 0, s, topk_ids, T, k, inv, counts);
-      launch(k_chunk_place, dim3(chunks), dim3(512), (size_t)E * 12, s, topk_ids, T, E, k, counts, offsets, perm, inv);
+      launch(k_chunk_scan, dim3((unsigned)E), dim3(256), 0, s, topk_ids, T, k, C, inv, counts);
+      launch(k_chunk_place, dim3(chunks), dim3(E <= 256 ? 256 : 512), (size_t)E * 12, s, topk_ids, T, E, k, C, counts,
+             offsets, perm, inv);
     }
   }
   if (err != hipSuccess) return set_error(MOE_EHIP, "moe_route_scored_permute: %s", hipGetErrorString(err));
