@@ -74,6 +74,10 @@ class LayerState:
         if logits is None:
             L.moe_router_logits(x, w_router, T, lay.H, lay.E, self.logits, stream)
             logits = self.logits
+        if lay.router is not None:
+            L.moe_route_scored_permute(lay.router, logits, T, lay.E, lay.k, self.ids, self.w, self.counts,
+                                       self.offsets, self.perm, self.inv, stream)
+            return
         L.moe_route_permute(logits, T, lay.E, lay.k, lay.renormalize, self.ids, self.w, self.counts, self.offsets,
                             self.perm, self.inv, stream)
 
@@ -88,10 +92,15 @@ class LayerState:
         return la
 
     def call(self, T, x, *, logits=None, w_router=None, stream=None, la=None):
-        """One layer call: router logits (if w_router is given), then moe_layer."""
+        """One layer call: router logits (if w_router is given), then moe_layer, or with a
+        scored router its routing and moe_expert_ffn."""
         if logits is None:
             L.moe_router_logits(x, w_router, T, self.layer.H, self.layer.E, self.logits, stream)
             logits = self.logits
+        if self.layer.router is not None:
+            self.route(T, logits=logits, stream=stream)
+            L.moe_expert_ffn(la.ffn if la is not None else self.args(T, x), stream)
+            return
         L.moe_layer(la if la is not None else self.layer_args(T, x, logits), stream)
 
     def forward(self, x, *, logits=None, w_router=None, stream=None):
@@ -106,9 +115,10 @@ class MoELayer:
     """Fully resident layer: expert e's blob sits in slot e of an HBM slot pool."""
 
     def __init__(self, *, E, k, H, I, fmt, max_tokens, device="cuda", shared=False, amode="bf16",
-                 renormalize=True, num_slots=None):
+                 renormalize=True, num_slots=None, router=None):
+        """router: None (softmax top-k by `renormalize`), or a router() with scores, bias and groups."""
         self.E, self.k, self.H, self.I, self.fmt = E, k, H, I, fmt
-        self.amode, self.renormalize = amode, renormalize
+        self.amode, self.renormalize, self.router = amode, renormalize, router
         self.dev = torch.device(device)
         self.blob_bytes = L.moe_blob_bytes(fmt, H, I)
         self.stride = (self.blob_bytes + 255) // 256 * 256
@@ -136,6 +146,89 @@ class MoELayer:
                     "forward", "check", "call", "layer_args"):
             return getattr(self.__dict__["state"], name)
         raise AttributeError(name)
+
+
+class DenseLayer:
+    """The dense layer that stands where a sparse one could: residual addition
+    and RMS norm, then a SwiGLU FFN whose products run on moe_linear, its
+    output added to the residual.
+
+        r = x + residual;  out = r + W_down (silu(W_gate n) * (W_up n)),  n = norm(r)
+
+    fmt "bf16": bf16 operands; "fp8" / "mxfp8": 8-bit rows on both sides, the
+    norm writing the first product's and moe_quantize_fp8 the second's.
+    Weights: gate_up [2 I, H] (the I gate rows, then the I up rows) and down
+    [H, I], bf16 or E4M3 codes with their scales (fp32 [rows], or E8M0
+    [cols / 128, rows, 4])."""
+
+    def __init__(self, *, H, I, fmt, max_tokens, norm_weight, gate_up, down, gate_up_scale=None, down_scale=None,
+                 eps=1e-6, device="cuda"):
+        dev, T = torch.device(device), max(max_tokens, 1)
+        self.H, self.I, self.fmt, self.max_tokens, self.eps = H, I, fmt, T, eps
+        self.norm_weight, self.gate_up, self.down = norm_weight, gate_up, down
+        self.gate_up_scale, self.down_scale = gate_up_scale, down_scale
+        bf16 = lambda n: torch.empty((T, n), dtype=torch.bfloat16, device=dev)  # noqa: E731
+        self.residual, self.h, self.out = bf16(H), bf16(I), bf16(H)
+        if fmt == "bf16":
+            self.n = bf16(H)
+        else:
+            self.q = torch.empty(T * max(H, I), dtype=torch.uint8, device=dev)
+            self.q_scale = torch.empty(T * max(H, I) if fmt == "mxfp8" else 4 * T, dtype=torch.uint8, device=dev)
+        # one workspace for every batch up to max_tokens: a captured call keeps its address
+        self._products = {}
+        self._ws = None
+        need = 0
+        for a in self._linear(T):
+            for a.T in range(1, T + 1):
+                need = max(need, L.moe_linear_workspace_size(a))
+        self._ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+
+    def _rows(self, T, n):
+        """8-bit rows of n columns in the layer's buffers: (codes, scales)."""
+        s = (self.q_scale[:T * n // 32].view(n // 128, T, 4) if self.fmt == "mxfp8" else
+             self.q_scale[:4 * T].view(torch.float32))
+        return self.q[:T * n].view(T, n), s
+
+    def _linear(self, T):
+        """Arguments of the two products for T tokens; the second's residual is set by the call."""
+        quant = self.fmt != "bf16"
+        nq, ns = self._rows(T, self.H) if quant else (self.n[:T], None)
+        hq, hs = self._rows(T, self.I) if quant else (self.h[:T], None)
+        up = L.linear_args(x=nq, w=self.gate_up, fmt=self.fmt, x_scale=ns, w_scale=self.gate_up_scale, act="silu",
+                           gated=True, out=self.h[:T])
+        down = L.linear_args(x=hq, w=self.down, fmt=self.fmt, x_scale=hs, w_scale=self.down_scale,
+                             residual=self.residual[:T], out=self.out[:T])
+        if self._ws is not None:
+            for a in (up, down):
+                a.workspace, a.workspace_bytes = self._ws.data_ptr(), self._ws.numel()
+        return up, down
+
+    def forward(self, x, residual=None, stream=None):
+        """x [T,H] and residual [T,H] or None, bf16; returns out [T,H] (the layer's buffer; the sum that
+        goes on is in it)."""
+        T = x.shape[0]
+        assert T <= self.max_tokens
+        if T == 0:
+            return self.out[:0]
+        if T not in self._products:
+            self._products[T] = self._linear(T)
+        up, down = self._products[T]
+        quant = self.fmt != "bf16"
+        nq, ns = self._rows(T, self.H) if quant else (self.n[:T], None)
+        norm = L.norm_args(x=x, weight=self.norm_weight, eps=self.eps, residual=residual,
+                           residual_out=None if residual is None else self.residual[:T],
+                           **({"q": nq, "q_scale": ns, "qmode": self.fmt} if quant else {"out": nq}))
+        L.moe_rmsnorm(norm, stream)
+        L.moe_linear(up, stream)
+        if quant:
+            hq, hs = self._rows(T, self.I)
+            L.moe_quantize_fp8(self.h[:T], T, self.I, self.fmt, hq, hs, stream)
+        if residual is None:  # the sum is x itself
+            down.residual, down.ldr = norm.x, norm.ldx
+        else:
+            down.residual, down.ldr = self.residual.data_ptr(), self.H
+        L.moe_linear(down, stream)
+        return self.out[:T]
 
 
 class CachedDecoder:

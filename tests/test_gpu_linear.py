@@ -228,6 +228,30 @@ def test_linear_mxfp8_far_scales(m, T, out):
     assert torch.all((o.cpu().double() - want).abs() <= tol + want.abs() * (2.0 ** -8 if out == "bf16" else U))
 
 
+@pytest.mark.gpu
+def test_fp8_instruction_cuts_small_products(m):
+    """The rule behind the tolerance of bf16 outputs: of 8 neighbouring products, two of 2^16 that cancel
+    and a small one, what is left is the small one within 2^-13 of 2^16; in a group of its own it is whole."""
+    need_gpu()
+    T, N, K = 64, 64, 128
+    small = torch.tensor([2.0 ** (i % 10 - 4) for i in range(T)])
+    for at, off in ((2, 2.0 ** 3), (7, 2.0 ** 3), (8, 0.0), (100, 0.0)):
+        x, w = torch.zeros(T, K), torch.zeros(N, K)
+        x[:, :2], w[:, 0], w[:, 1] = 256.0, 256.0, -256.0
+        x[:, at], w[:, at] = small, 2.0
+        ones = torch.ones(64, device=DEV)
+        o = torch.empty((T, N), dtype=torch.bfloat16, device=DEV)
+        a = m.linear_args(x=x.to(torch.float8_e4m3fn).to(DEV), w=w.to(torch.float8_e4m3fn).to(DEV), fmt="fp8",
+                          x_scale=ones, w_scale=ones, out=o)
+        n = m.moe_linear_workspace_size(a)
+        ws = torch.empty(max(n, 16), dtype=torch.uint8, device=DEV)
+        a.workspace, a.workspace_bytes = ws.data_ptr(), n
+        say("fp8 products, small one at", at)
+        m.moe_linear(a)
+        torch.cuda.synchronize()
+        assert torch.all((o.cpu().float() - 2 * small[:, None]).abs() <= off)
+
+
 def _ok(L, **kw):
     a = dict(T=4, N=32, K=128, x=0x10000, w=0x20000, out=0x30000)
     a.update(kw)
