@@ -150,6 +150,7 @@ SIGNATURES = {
     "moe_cache_mark_used": (_i, [_vp, _vp, _i, _vp]),
     "moe_cache_reset": (_i, [_vp]),
     "moe_cache_use_copy_engine": (_i, [_vp, _i]),
+    "moe_cache_use_router": (_i, [_vp, _i, ctypes.POINTER(Router)]),
     "moe_cache_pin_resident": (_i, [_vp, _i, _i]),
     "moe_cache_stats": (_i, [_vp, _vp, _vp, _vp]),
     "moe_cache_map_bytes": (_sz, [_i]),
@@ -592,6 +593,15 @@ def moe_cache_reset(cache: Cache):
 
 def moe_cache_use_copy_engine(cache: Cache, on: bool):
     _check(lib().moe_cache_use_copy_engine(cache.handle, 1 if on else 0), "moe_cache_use_copy_engine")
+
+
+def moe_cache_use_router(cache: Cache, layer: int, r: Router | None):
+    """Steps of `layer` (-1: every layer) route by the scored router r (None: softmax top-k again)."""
+    if r is not None:
+        cache._routers = getattr(cache, "_routers", {})
+        cache._routers[layer] = r  # its bias stays alive with the cache
+    _check(lib().moe_cache_use_router(cache.handle, int(layer), None if r is None else ctypes.byref(r)),
+           "moe_cache_use_router")
 
 
 def moe_cache_pin_resident(cache: Cache, layer, s0):

@@ -39,6 +39,7 @@
 #include <vector>
 
 #include "host_common.h"
+#include "route_hook.h"
 
 namespace moe {
 hipError_t launch_move_slots(const int32_t* src_slots, int n, int dst0, const void* src_pool, void* dst_pool,
@@ -93,6 +94,13 @@ struct moe_cache {
   // hit_done joins them back before the combine (copy_engine: 1 forces the
   // copy-engine fills instead)
   int copy_engine = 0;
+  // the layers' routers (moe_cache_use_router); empty: moe_route in every layer
+  moe::RouteHook route_hook = nullptr;
+  std::vector<moe_router> routers;
+  std::vector<uint8_t> has_router;
+  const moe_router* router(int layer) const {
+    return route_hook && has_router[layer] ? &routers[layer] : nullptr;
+  }
   hipStream_t side = nullptr;
   hipEvent_t hit_done = nullptr;
   void* side_map = nullptr;
@@ -380,6 +388,21 @@ extern "C" moe_status moe_cache_use_copy_engine(moe_cache* c, int on) {
   return MOE_OK;
 }
 
+void moe::cache_shape(const moe_cache* c, int* num_layers, int* num_experts) {
+  *num_layers = c->num_layers;
+  *num_experts = c->num_experts;
+}
+
+void moe::cache_set_router(moe_cache* c, int layer, const moe_router* r, RouteHook hook) {
+  c->routers.resize(c->num_layers);
+  c->has_router.resize(c->num_layers, 0);
+  c->route_hook = hook;
+  for (int l = layer < 0 ? 0 : layer; l < (layer < 0 ? c->num_layers : layer + 1); ++l) {
+    c->has_router[l] = r ? 1 : 0;
+    if (r) c->routers[l] = *r;
+  }
+}
+
 extern "C" moe_status moe_cache_mark_used(moe_cache* c, const int32_t* slots, int n, moe_stream_t compute_stream) {
   MOE_CHECK_ARG(c && (n == 0 || slots), "moe_cache_mark_used: null pointer");
   for (int i = 0; i < n; ++i)
@@ -619,17 +642,27 @@ static moe_status decode_step(moe_cache* c, moe_cache_step* s, moe_hybrid* hy, m
     // the routing writes the counts into the mapped host buffer and then
     // publishes the step's number; the host polls for it
     const uint32_t seq = ++c->seq;
-    st = moe::route_permute_publish(s->logits, T, E, f.k, s->renormalize, s->topk_ids, const_cast<float*>(f.topk_w),
-                                    const_cast<int32_t*>(f.counts), const_cast<int32_t*>(f.offsets),
-                                    const_cast<int32_t*>(f.perm), const_cast<int32_t*>(f.inv), counts_dev, c->flag_dev,
-                                    seq, ks);
+    if (const moe_router* r = c->router(s->layer))
+      st = c->route_hook(r, s->logits, T, E, f.k, s->topk_ids, const_cast<float*>(f.topk_w),
+                         const_cast<int32_t*>(f.counts), const_cast<int32_t*>(f.offsets), const_cast<int32_t*>(f.perm),
+                         const_cast<int32_t*>(f.inv), counts_dev, c->flag_dev, seq, ks);
+    else
+      st = moe::route_permute_publish(s->logits, T, E, f.k, s->renormalize, s->topk_ids, const_cast<float*>(f.topk_w),
+                                      const_cast<int32_t*>(f.counts), const_cast<int32_t*>(f.offsets),
+                                      const_cast<int32_t*>(f.perm), const_cast<int32_t*>(f.inv), counts_dev,
+                                      c->flag_dev, seq, ks);
     if (st != MOE_OK) return st;
     st = wait_flag(c, seq, ks, who);
     if (st != MOE_OK) return st;
   } else {
-    st = moe_route_permute(s->logits, T, E, f.k, s->renormalize, s->topk_ids, const_cast<float*>(f.topk_w),
-                           const_cast<int32_t*>(f.counts), const_cast<int32_t*>(f.offsets), const_cast<int32_t*>(f.perm),
-                           const_cast<int32_t*>(f.inv), compute_stream);
+    if (const moe_router* r = c->router(s->layer))
+      st = c->route_hook(r, s->logits, T, E, f.k, s->topk_ids, const_cast<float*>(f.topk_w),
+                         const_cast<int32_t*>(f.counts), const_cast<int32_t*>(f.offsets), const_cast<int32_t*>(f.perm),
+                         const_cast<int32_t*>(f.inv), nullptr, nullptr, 0, ks);
+    else
+      st = moe_route_permute(s->logits, T, E, f.k, s->renormalize, s->topk_ids, const_cast<float*>(f.topk_w),
+                             const_cast<int32_t*>(f.counts), const_cast<int32_t*>(f.offsets),
+                             const_cast<int32_t*>(f.perm), const_cast<int32_t*>(f.inv), compute_stream);
     if (st != MOE_OK) return st;
     MOE_HIP(hipMemcpyAsync(s->host_counts, f.counts, sizeof(int32_t) * (size_t)E, hipMemcpyDeviceToHost, ks));
     if (hy) {
@@ -892,7 +925,11 @@ extern "C" moe_status moe_cache_prefill_step(moe_cache* c, moe_cache_prefill* s,
   for (int e = 0; e < E; ++e)
     if ((st = wait_fill(c, c->step_slot[e], ks)) != MOE_OK) return st;
   if (T > 0) {
-    if ((long long)T * f.k <= 1024) {
+    if (const moe_router* r = c->router(s->layer)) {
+      st = c->route_hook(r, s->logits, T, E, f.k, s->topk_ids, const_cast<float*>(f.topk_w),
+                         const_cast<int32_t*>(f.counts), const_cast<int32_t*>(f.offsets), const_cast<int32_t*>(f.perm),
+                         const_cast<int32_t*>(f.inv), nullptr, nullptr, 0, ks);
+    } else if ((long long)T * f.k <= 1024) {
       st = moe_route_permute(s->logits, T, E, f.k, s->renormalize, s->topk_ids, const_cast<float*>(f.topk_w),
                              const_cast<int32_t*>(f.counts), const_cast<int32_t*>(f.offsets),
                              const_cast<int32_t*>(f.perm), const_cast<int32_t*>(f.inv), compute_stream);

@@ -23,6 +23,7 @@
 #include <type_traits>
 
 #include "common.h"
+#include "route_hook.h"
 #include "topk.h"
 #include "wave.h"
 
@@ -865,5 +866,33 @@ extern "C" moe_status moe_route_scored_permute(const moe_router* r, const float*
   }
   if (err != hipSuccess) return set_error(MOE_EHIP, "moe_route_scored_permute: %s", hipGetErrorString(err));
   MOE_LAUNCHED();
+  return MOE_OK;
+}
+
+namespace {
+
+moe_status route_of_cache(const moe_router* r, const float* logits, int T, int E, int k, int32_t* topk_ids,
+                          float* topk_w, int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv,
+                          int32_t* host_counts, uint32_t* flag, uint32_t seq, hipStream_t s) {
+  moe_status st = moe_route_scored_permute(r, logits, T, E, k, topk_ids, topk_w, counts, offsets, perm, inv,
+                                           reinterpret_cast<moe_stream_t>(s));
+  if (st != MOE_OK || !host_counts) return st;
+  const hipError_t e = launch_publish_counts(counts, E, host_counts, flag, seq, s);
+  if (e != hipSuccess) return set_error(MOE_EHIP, "count handoff launch failed: %s", hipGetErrorString(e));
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" moe_status moe_cache_use_router(moe_cache* c, int layer, const moe_router* r) {
+  MOE_CHECK_ARG(c, "moe_cache_use_router: null cache");
+  int layers = 0, experts = 0;
+  cache_shape(c, &layers, &experts);
+  MOE_CHECK_ARG(layer >= -1 && layer < layers, "moe_cache_use_router: layer %d out of range", layer);
+  if (r) {
+    const moe_status st = check_router("moe_cache_use_router", r, 0, experts, 1);
+    if (st != MOE_OK) return st;
+  }
+  cache_set_router(c, layer, r, route_of_cache);
   return MOE_OK;
 }

@@ -231,6 +231,14 @@ class DenseLayer:
         return self.out[:T]
 
 
+def _use_routers(cache, router):
+    """Sets a cache's scored routers: one for every layer, or a list of one a layer."""
+    if router is None:
+        return
+    for l, r in enumerate(router) if isinstance(router, (list, tuple)) else [(-1, router)]:
+        L.moe_cache_use_router(cache, l, r)
+
+
 class CachedDecoder:
     """Decode through the expert-slot cache: `num_layers` layers of `num_experts`
     experts whose blobs sit in a pinned host bank, `num_slots` HBM slots shared
@@ -244,10 +252,11 @@ class CachedDecoder:
     the host with `host_threads` threads, not cached).
     copy_engine: copy misses through the copy engine on the side stream even
     where a fill kernel on the compute stream could copy them.
+    router: None (softmax top-k), a router() for every layer, or a list of one a layer.
     """
 
     def __init__(self, *, num_layers, num_experts, k, H, I, fmt, num_slots, host_blob, max_tokens=1,
-                 device="cuda", renormalize=True, copy_ratio=None, host_threads=8, copy_engine=False):
+                 device="cuda", renormalize=True, copy_ratio=None, host_threads=8, copy_engine=False, router=None):
         self.L, self.E, self.k, self.H, self.I, self.fmt = num_layers, num_experts, k, H, I, fmt
         self.dev = torch.device(device)
         self.blob_bytes = L.moe_blob_bytes(fmt, H, I)
@@ -256,6 +265,7 @@ class CachedDecoder:
         self.cache = L.moe_cache_create(num_slots, self.stride, self.pool, num_layers, num_experts)
         if copy_engine:
             L.moe_cache_use_copy_engine(self.cache, True)
+        _use_routers(self.cache, router)
         self.copy_stream = torch.cuda.Stream(device=self.dev)
         self._copy_handle = self.copy_stream.cuda_stream
         T, E = max(max_tokens, 1), num_experts
@@ -398,10 +408,11 @@ class CachedPrefill:
     computing and the layer arriving).
 
     host_blob(layer, e) -> pinned uint8 tensor holding that expert's blob.
+    router: None (softmax top-k), a router() for every layer, or a list of one a layer.
     """
 
     def __init__(self, *, num_layers, num_experts, k, H, I, fmt, max_tokens, host_blob, amode="bf16",
-                 num_slots=None, device="cuda", renormalize=True):
+                 num_slots=None, device="cuda", renormalize=True, router=None):
         self.L, self.E, self.k, self.H, self.I, self.fmt, self.amode = num_layers, num_experts, k, H, I, fmt, amode
         self.renormalize = 1 if renormalize else 0
         self.dev = torch.device(device)
@@ -410,6 +421,7 @@ class CachedPrefill:
         self.num_slots = num_slots or 2 * num_experts
         self.pool = torch.empty(self.num_slots * self.stride, dtype=torch.uint8, device=self.dev)
         self.cache = L.moe_cache_create(self.num_slots, self.stride, self.pool, num_layers, num_experts)
+        _use_routers(self.cache, router)
         self.copy_stream = torch.cuda.Stream(device=self.dev)
         E, T = num_experts, max(max_tokens, 1)
         self.max_tokens = T

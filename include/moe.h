@@ -477,6 +477,12 @@ moe_status moe_cache_mark_used(moe_cache* c, const int32_t* slots, int n, moe_st
  * default).  Both orders give the same results and trace. */
 moe_status moe_cache_use_copy_engine(moe_cache* c, int on);
 
+/* Decode and prefill steps of `layer` (-1: of every layer) route by *r
+ * (moe_route_scored_permute; the step's renormalize is not used) instead of
+ * moe_route; r null: by moe_route again.  *r is copied; its bias has to stay
+ * valid.  Takes effect with the next step. */
+moe_status moe_cache_use_router(moe_cache* c, int layer, const moe_router* r);
+
 /* Hits, misses and bytes copied by cache_fill since creation or reset (host). */
 moe_status moe_cache_stats(const moe_cache* c, long long* hits, long long* misses, long long* bytes_filled);
 

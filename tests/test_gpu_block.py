@@ -208,3 +208,67 @@ def test_two_streams_at_once(m):
             torch.cuda.current_stream().wait_stream(s)
         torch.cuda.synchronize()
         assert all(torch.equal(outs[i], wants[i]) for i in range(2))
+
+
+@pytest.mark.parametrize("copy_engine", [False, True])
+@pytest.mark.parametrize("T", [1, 3])
+def test_cached_decode_with_routers(m, T, copy_engine):
+    """The cached decode stream with a scored router a layer: the step's experts are the rule's, the
+    outputs the oracle's."""
+    from fp4_expert_ffn_amd.layer import CachedDecoder, to_numpy_bf16
+    from tests.test_gpu_cache import _pinned_blob
+    layers, E, k, H, I, tokens = 2, 16, 4, 256, 128, 10
+    stride = (m.moe_blob_bytes("nvfp4", H, I) + 255) // 256 * 256
+    experts = {(l, e): synth.expert("nvfp4", H, I, config=78, layer=l, expert_id=e) for l in range(layers) for e in range(E)}
+    bank = {key: _pinned_blob(ex, stride) for key, ex in experts.items()}
+    bias = (np.random.default_rng(1).standard_normal(E) * 0.1).astype(np.float32)
+    kws = [dict(ROUTER), dict(score="softmax", n_group=2, topk_group=1, group_rank="max", renormalize=False)]
+    routers = [m.router(bias=torch.from_numpy(bias).to(DEV), **kw) for kw in kws]
+    dec = CachedDecoder(num_layers=layers, num_experts=E, k=k, H=H, I=I, fmt="nvfp4", num_slots=20, max_tokens=T,
+                        host_blob=lambda l, e: bank[l, e], device=DEV, copy_engine=copy_engine, router=routers)
+    rng = np.random.default_rng(9)
+    say(f"cached decode with routers T={T} copy_engine={copy_engine}")
+    for t in range(tokens):
+        for l in range(layers):
+            logits = rng.standard_normal((T, E)).astype(np.float32)
+            x = synth.f32_to_bf16_bits(rng.standard_normal((T, H)).astype(np.float32))
+            out, trace = dec.step(l, torch.from_numpy(x.view(np.int16)).to(DEV), torch.from_numpy(logits).to(DEV))
+            torch.cuda.synchronize()
+            ids, w = rule(logits, k, bias=bias, **kws[l])
+            assert np.array_equal(dec.ids[:T].cpu().numpy(), ids)
+            assert trace[0].tolist() == sorted(set(ids.reshape(-1).tolist()))
+            ref = oracle.moe.layer_outputs(x, ids, dec.w[:T].cpu().numpy(), E,
+                                           lambda e: oracle.moe.dequant_expert(experts[l, e]))
+            assert oracle.moe.relative_error(synth.bf16_bits_to_f32(to_numpy_bf16(out)), ref) <= 1e-2
+    # back to the softmax routing
+    m.moe_cache_use_router(dec.cache, -1, None)
+    logits = rng.standard_normal((T, E)).astype(np.float32)
+    dec.step(0, torch.from_numpy(x.view(np.int16)).to(DEV), torch.from_numpy(logits).to(DEV))
+    torch.cuda.synchronize()
+    assert np.array_equal(dec.ids[:T].cpu().numpy(), oracle.moe.route(logits, k)[0])
+    dec.close()
+
+
+def test_cached_prefill_with_a_router(m):
+    from fp4_expert_ffn_amd.layer import CachedPrefill, to_numpy_bf16
+    from tests.test_gpu_cache import _pinned_blob
+    layers, E, k, H, I, T = 2, 8, 2, 256, 128, 90
+    stride = (m.moe_blob_bytes("nvfp4", H, I) + 255) // 256 * 256
+    experts = {(l, e): synth.expert("nvfp4", H, I, config=79, layer=l, expert_id=e) for l in range(layers) for e in range(E)}
+    bank = {key: _pinned_blob(ex, stride) for key, ex in experts.items()}
+    kw = dict(score="sigmoid", scale=1.5)
+    pf = CachedPrefill(num_layers=layers, num_experts=E, k=k, H=H, I=I, fmt="nvfp4", max_tokens=T,
+                       host_blob=lambda l, e: bank[l, e], device=DEV, router=m.router(**kw))
+    rng = np.random.default_rng(10)
+    logits = rng.standard_normal((layers, T, E)).astype(np.float32)
+    x = synth.f32_to_bf16_bits(rng.standard_normal((layers, T, H)).astype(np.float32))
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(DEV)  # noqa: E731
+    outs = [torch.empty((T, H), dtype=torch.int16, device=DEV) for _ in range(layers)]
+    say("cached prefill with a router")
+    pf.run([dev(x[l].view(np.int16)) for l in range(layers)], [dev(logits[l]) for l in range(layers)], outs)
+    torch.cuda.synchronize()
+    for l in range(layers):
+        ids, w = rule(logits[l], k, **kw)
+        ref = oracle.moe.layer_outputs(x[l], ids, w, E, lambda e: oracle.moe.dequant_expert(experts[l, e]))
+        assert oracle.moe.relative_error(synth.bf16_bits_to_f32(to_numpy_bf16(outs[l])), ref) <= 1e-2
+    pf.close()

@@ -262,3 +262,15 @@ def test_route_refuses_nulls_and_bad_biases(m):
     for bias in (torch.zeros(64), torch.zeros(64, dtype=torch.float64)):
         with pytest.raises(m.MoeError):
             m.router(bias=bias)
+
+
+def test_cache_router_refusals(m):
+    c = m.moe_cache_create(4, 1 << 20, 0, 2, 16)
+    for layer, kw, msg in ((2, {}, "layer 2"), (-2, {}, "layer -2"), (0, dict(n_group=3), "n_group"),
+                           (0, dict(score=9), "score")):
+        with pytest.raises(m.MoeError) as e:
+            m.moe_cache_use_router(c, layer, m.router(**kw))
+        assert e.value.status == 1 and msg in str(e.value)
+    m.moe_cache_use_router(c, -1, m.router(score="sigmoid", n_group=4, topk_group=2))
+    m.moe_cache_use_router(c, 1, None)
+    c.close()
