@@ -450,21 +450,38 @@ def router(*, score="softmax", n_group=1, topk_group=1, group_rank="max", renorm
     return t.done(r)
 
 
-def _check_router(r: Router, E: int, what: str):
+def _check_route(what: str, r: Router, E: int, *tensors):
+    """The router's bias fits E, and each (name, tensor, type, values) is dense, of its type and long enough."""
+    import torch
     n = getattr(r, "_experts", None)
     if n is not None and n != E:
         _bad(f"{what}: the router's bias has {n} experts, E={E}")
+    d = None
+    for name, t, kind, need in tensors:
+        if t is None or isinstance(t, int):
+            continue
+        if t.dtype is not getattr(torch, kind) or not t.is_contiguous() or t.numel() < need or not t.is_cuda:
+            _bad(f"{what}: {name} must be a dense {kind} GPU tensor of at least {need} values")
+        d = t.device.index if d is None else d
+        if t.device.index != d:
+            _bad(f"{what}: {name} is on {t.device}, other arguments on cuda:{d}")
+    if d is not None and d != torch.cuda.current_device():
+        _bad(f"{what}: tensors on cuda:{d}, current device cuda:{torch.cuda.current_device()}")
     _current(r, what)
 
 
 def moe_route_scored(r: Router, logits, T, E, k, topk_ids, topk_w, stream=None):
-    _check_router(r, E, "moe_route_scored")
+    _check_route("moe_route_scored", r, E, ("logits", logits, "float32", T * E), ("topk_ids", topk_ids, "int32", T * k),
+                 ("topk_w", topk_w, "float32", T * k))
     _check(lib().moe_route_scored(ctypes.byref(r), ptr(logits), T, E, k, ptr(topk_ids), ptr(topk_w),
                                   stream_handle(stream)), "moe_route_scored")
 
 
 def moe_route_scored_permute(r: Router, logits, T, E, k, topk_ids, topk_w, counts, offsets, perm, inv, stream=None):
-    _check_router(r, E, "moe_route_scored_permute")
+    _check_route("moe_route_scored_permute", r, E, ("logits", logits, "float32", T * E),
+                 ("topk_ids", topk_ids, "int32", T * k), ("topk_w", topk_w, "float32", T * k),
+                 ("counts", counts, "int32", E), ("offsets", offsets, "int32", E + 1), ("perm", perm, "int32", T * k),
+                 ("inv", inv, "int32", T * k))
     _check(lib().moe_route_scored_permute(ctypes.byref(r), ptr(logits), T, E, k, ptr(topk_ids), ptr(topk_w),
                                           ptr(counts), ptr(offsets), ptr(perm), ptr(inv), stream_handle(stream)),
            "moe_route_scored_permute")

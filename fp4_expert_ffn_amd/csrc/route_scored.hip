@@ -788,14 +788,6 @@ RouterP router_params(const moe_router* r, const float* logits, int E) {
   return R;
 }
 
-// More than 64 KiB of dynamic LDS: asked for on each call (a few ns), for the device that is current.
-template <typename K>
-hipError_t allow_lds(K kernel, size_t bytes) {
-  if (bytes <= 48 * 1024) return hipSuccess;
-  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)bytes);
-}
-
 }  // namespace
 
 extern "C" moe_status moe_route_scored(const moe_router* r, const float* logits, int T, int E, int k,
@@ -832,7 +824,7 @@ extern "C" moe_status moe_route_scored_permute(const moe_router* r, const float*
   }
   RouterP R = router_params(r, logits, E);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  hipError_t err = hipSuccess;
+  // dynamic LDS below: at most 48 KiB (E = 1024 by 64 x 16, eight rows in work)
   if (T <= kChunk) {
     with_shape(R, E, T <= 16, [&](auto lr, auto npl) {
       constexpr int LR = decltype(lr)::value, NPL = decltype(npl)::value, RPW = 64 / LR;
@@ -840,8 +832,6 @@ extern "C" moe_status moe_route_scored_permute(const moe_router* r, const float*
       // (at least) four waves for the scan over the experts
       const int nw = std::max(waves, std::min(4, (E + 63) / 64));
       const size_t lds = (size_t)E * 12 + (size_t)(nw * RPW + 1) * E * sizeof(float);
-      err = allow_lds(k_route_one<LR, NPL>, lds);
-      if (err != hipSuccess) return;
       launch(k_route_one<LR, NPL>, dim3(1), dim3((unsigned)(64 * nw)), lds, s, R, logits, T, E, k, topk_ids, topk_w,
              counts, offsets, perm, inv);
     });
@@ -853,18 +843,13 @@ extern "C" moe_status moe_route_scored_permute(const moe_router* r, const float*
       constexpr int LR = decltype(lr)::value, NPL = decltype(npl)::value;
       const int nt = std::min(kMaxThreads<LR, NPL>, C * LR);
       const size_t lds = (size_t)E * 4 + (size_t)(nt / LR + 1) * E * sizeof(float);
-      err = allow_lds(k_route_chunk<LR, NPL>, lds);
-      if (err != hipSuccess) return;
       launch(k_route_chunk<LR, NPL>, dim3(chunks), dim3((unsigned)nt), lds, s, R, logits, T, E, k, C, topk_ids, topk_w,
              inv);
     });
-    if (err == hipSuccess) {
-      launch(k_chunk_scan, dim3((unsigned)E), dim3(256), 0, s, topk_ids, T, k, C, inv, counts);
-      launch(k_chunk_place, dim3(chunks), dim3(E <= 256 ? 256 : 512), (size_t)E * 12, s, topk_ids, T, E, k, C, counts,
-             offsets, perm, inv);
-    }
+    launch(k_chunk_scan, dim3((unsigned)E), dim3(256), 0, s, topk_ids, T, k, C, inv, counts);
+    launch(k_chunk_place, dim3(chunks), dim3(E <= 256 ? 256 : 512), (size_t)E * 12, s, topk_ids, T, E, k, C, counts,
+           offsets, perm, inv);
   }
-  if (err != hipSuccess) return set_error(MOE_EHIP, "moe_route_scored_permute: %s", hipGetErrorString(err));
   MOE_LAUNCHED();
   return MOE_OK;
 }

@@ -347,7 +347,10 @@ typedef struct {
  *   r = x + residual (fp32; residual_out is r rounded once),
  *   y = r * weight / sqrt(mean(r^2) + eps)   (from the unrounded r),
  * written as bf16 (out) and as 8-bit rows (q, q_scale), both rounded from
- * the fp32 y.  One of out, q and residual_out at least.
+ * the fp32 y.  One of out, q and residual_out at least.  The sum of squares
+ * is held in fp32: where it passes that range (values above about 1.8e19 /
+ * sqrt(H)) the finite values of the row become 0, and squares of values below
+ * about 1e-19 lose bits, which shows only where eps does not cover them.
  * Errors: MOE_EINVAL (sizes, strides, null or misaligned pointers);
  * nothing is enqueued on an error. */
 moe_status moe_rmsnorm(const moe_norm_args* a, moe_stream_t stream);
@@ -402,7 +405,13 @@ size_t moe_linear_workspace_size(const moe_linear_args* a);
 
 /* out = fn(x W^T + bias) + residual, or fn(x W_g^T + b_g) * (x W_u^T + b_u) +
  * residual: products of the exact operands summed in fp32, the epilogue in
- * fp32, one rounding to out's type.
+ * fp32, one rounding to out's type.  E4M3 operands with bf16 outputs run on
+ * the FP8 matrix instructions, which add 8 neighbouring products at once and
+ * drop each one's bits below 2^-13 of the largest of the 8.  With fp32 outputs
+ * they are decoded to bf16 instead: every product exact, all sums in fp32 (and
+ * block scales outside 2^-117 .. 2^119 leave the range of the decoded values).
+ * A block scale of code 255 (NaN), which no encoder here writes, gives no
+ * defined sums.
  * [page "FreeToken qwen：...", 3rd paragraph: the layer's products; the dense
  *  product beside the experts and its epilogue are this library's reading.]
  * Requires T >= 0, N >= 1, K >= 1, rows of whole 16-byte pieces (K % 8 == 0

@@ -264,6 +264,17 @@ def test_route_refuses_nulls_and_bad_biases(m):
             m.router(bias=bias)
 
 
+def test_route_refuses_tensors(m):
+    """Strided, short or mistyped tensors and tensors outside the GPU never reach the kernels."""
+    lg = torch.zeros(4, 64)
+    i, w = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    for bad in ((lg.double(), i, w), (lg.t().contiguous().t(), i, w), (lg[:3], i, w), (lg, i.long(), w), (lg, i, w[:1]),
+                (lg, i, w)):
+        with pytest.raises(m.MoeError) as e:
+            m.moe_route_scored(m.router(), bad[0], 4, 64, 2, bad[1], bad[2], stream=0)
+        assert e.value.status == 1 and "dense" in str(e.value)
+
+
 def test_cache_router_refusals(m):
     c = m.moe_cache_create(4, 1 << 20, 0, 2, 16)
     for layer, kw, msg in ((2, {}, "layer 2"), (-2, {}, "layer -2"), (0, dict(n_group=3), "n_group"),
