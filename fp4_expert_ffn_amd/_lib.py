@@ -450,38 +450,40 @@ def router(*, score="softmax", n_group=1, topk_group=1, group_rank="max", renorm
     return t.done(r)
 
 
-def _check_route(what: str, r: Router, E: int, *tensors):
-    """The router's bias fits E, and each (name, tensor, type, values) is dense, of its type and long enough."""
+def _check_route(what: str, r: Router, E: int, floats, ints):
+    """The router's bias fits E; floats (fp32) and ints (int32), pairs of a tensor and its least length, are
+    dense and on the current device.  A decode step's routing takes 7 us: no names or strings before a fault."""
     import torch
     n = getattr(r, "_experts", None)
     if n is not None and n != E:
         _bad(f"{what}: the router's bias has {n} experts, E={E}")
-    d = None
-    for name, t, kind, need in tensors:
-        if t is None or isinstance(t, int):
-            continue
-        if t.dtype is not getattr(torch, kind) or not t.is_contiguous() or t.numel() < need or not t.is_cuda:
-            _bad(f"{what}: {name} must be a dense {kind} GPU tensor of at least {need} values")
-        d = t.device.index if d is None else d
-        if t.device.index != d:
-            _bad(f"{what}: {name} is on {t.device}, other arguments on cuda:{d}")
-    if d is not None and d != torch.cuda.current_device():
-        _bad(f"{what}: tensors on cuda:{d}, current device cuda:{torch.cuda.current_device()}")
-    _current(r, what)
+    dev = getattr(r, "_device", None)
+    for kind, pairs in ((torch.float32, floats), (torch.int32, ints)):
+        for t, need in pairs:
+            if t is None or t.__class__ is int:
+                continue
+            d = t.get_device()
+            if t.dtype is not kind or d < 0 or not t.is_contiguous() or t.numel() < need:
+                _bad(f"{what}: a {t.dtype} tensor of {t.numel()} values on {t.device} where a dense {kind} GPU "
+                     f"tensor of at least {need} values belongs")
+            if dev is None:
+                dev = d
+            elif d != dev:
+                _bad(f"{what}: tensors on cuda:{dev} and cuda:{d}")
+    if dev is not None and torch.cuda.current_device() != dev:
+        _bad(f"{what}: tensors on cuda:{dev}, current device cuda:{torch.cuda.current_device()}")
 
 
 def moe_route_scored(r: Router, logits, T, E, k, topk_ids, topk_w, stream=None):
-    _check_route("moe_route_scored", r, E, ("logits", logits, "float32", T * E), ("topk_ids", topk_ids, "int32", T * k),
-                 ("topk_w", topk_w, "float32", T * k))
+    _check_route("moe_route_scored", r, E, ((logits, T * E), (topk_w, T * k)), ((topk_ids, T * k),))
     _check(lib().moe_route_scored(ctypes.byref(r), ptr(logits), T, E, k, ptr(topk_ids), ptr(topk_w),
                                   stream_handle(stream)), "moe_route_scored")
 
 
 def moe_route_scored_permute(r: Router, logits, T, E, k, topk_ids, topk_w, counts, offsets, perm, inv, stream=None):
-    _check_route("moe_route_scored_permute", r, E, ("logits", logits, "float32", T * E),
-                 ("topk_ids", topk_ids, "int32", T * k), ("topk_w", topk_w, "float32", T * k),
-                 ("counts", counts, "int32", E), ("offsets", offsets, "int32", E + 1), ("perm", perm, "int32", T * k),
-                 ("inv", inv, "int32", T * k))
+    n = T * k
+    _check_route("moe_route_scored_permute", r, E, ((logits, T * E), (topk_w, n)),
+                 ((topk_ids, n), (counts, E), (offsets, E + 1), (perm, n), (inv, n)))
     _check(lib().moe_route_scored_permute(ctypes.byref(r), ptr(logits), T, E, k, ptr(topk_ids), ptr(topk_w),
                                           ptr(counts), ptr(offsets), ptr(perm), ptr(inv), stream_handle(stream)),
            "moe_route_scored_permute")
