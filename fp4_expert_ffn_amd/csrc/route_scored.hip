@@ -816,13 +816,25 @@ extern "C" moe_status moe_route_scored_permute(const moe_router* r, const float*
   MOE_CHECK_ARG((long long)T * k <= (1 << 17), "moe_route_scored_permute: T*k = %lld exceeds 131072", (long long)T * k);
   MOE_CHECK_ARG(counts && offsets && (T == 0 || (logits && topk_ids && topk_w && perm && inv)),
                 "moe_route_scored_permute: null pointer");
-  if (T == 0 || (T > kChunk && E > kChunk * k)) {
-    // nothing to route, or more experts than a chunk's part of inv has words for their counts
+  RouterP R = router_params(r, logits, E);
+  // the smallest chunk whose part of inv holds its counts: the most workgroups
+  const int C = E <= 16 * k ? 16 : (E <= 32 * k ? 32 : kChunk);
+  // A workgroup that takes its rows in several passes is late while others
+  // idle: routed by a launch of its own over all CUs, then permuted.  Before
+  // and after (us, k = 8): 64 tokens of 512 experts 27 -> 15, 1000 of 3 x 160
+  // 63 -> 21, of 200 experts (one pass) 16 -> 15, 4000 of 320 (4 passes) 33 ->
+  // 31; 4000 of 8 x 32 (one pass) 22 -> 24, 16384 of 512 41 -> 87.
+  int passes = 1;
+  with_shape(R, E, T <= 16, [&](auto lr, auto npl) {
+    const int rows = kMaxThreads<decltype(lr)::value, decltype(npl)::value> / decltype(lr)::value;
+    passes = (std::min(T, T <= kChunk ? kChunk : C) + rows - 1) / rows;
+  });
+  // or nothing to route, or more experts than a chunk's part of inv has words for their counts
+  if (T == 0 || (T > kChunk && E > kChunk * k) || (passes > 1 && T <= 1024 * passes)) {
     st = moe_route_scored(r, logits, T, E, k, topk_ids, topk_w, stream);
     if (st != MOE_OK) return st;
     return moe_permute(topk_ids, T, k, E, counts, offsets, perm, inv, stream);
   }
-  RouterP R = router_params(r, logits, E);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   // dynamic LDS below: at most 48 KiB (E = 1024 by 64 x 16, eight rows in work)
   if (T <= kChunk) {
@@ -836,8 +848,6 @@ extern "C" moe_status moe_route_scored_permute(const moe_router* r, const float*
              counts, offsets, perm, inv);
     });
   } else {
-    // the smallest chunk whose part of inv holds its counts: the most workgroups
-    const int C = E <= 16 * k ? 16 : (E <= 32 * k ? 32 : kChunk);
     const unsigned chunks = (unsigned)((T + C - 1) / C);
     with_shape(R, E, false, [&](auto lr, auto npl) {
       constexpr int LR = decltype(lr)::value, NPL = decltype(npl)::value;

@@ -209,6 +209,21 @@ def test_route_long_batches(m, T, E, k):
     assert np.array_equal(gv[gp], np.arange(T * k))
 
 
+# Both sides of where a batch is routed by a launch of its own: rows a workgroup takes at once, 1024 tokens a pass.
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,k,G", [(8, 480, 8, 3), (9, 480, 8, 3), (16, 320, 8, 1), (17, 320, 8, 1), (32, 200, 8, 1),
+                                     (33, 200, 8, 1), (64, 512, 8, 1), (65, 512, 8, 1), (2048, 210, 8, 3),
+                                     (2049, 210, 8, 3), (4096, 320, 8, 1), (4097, 320, 8, 1), (8192, 480, 8, 3),
+                                     (8193, 480, 8, 3), (2049, 200, 3, 1), (5, 1000, 16, 8), (4, 1000, 16, 8)])
+def test_route_split_batches(m, T, E, k, G):
+    need_gpu()
+    rng = np.random.default_rng(T + E)
+    logits = (rng.standard_normal((T, E)) * 1.5).astype(np.float32)
+    bias = (rng.standard_normal(E) * 0.1).astype(np.float32)
+    check(m, logits, k, score="sigmoid", n_group=G, topk_group=max(1, G - 1), group_rank="top2" if G > 1 else "max",
+          bias=bias)
+
+
 @pytest.mark.gpu
 def test_route_no_tokens(m):
     need_gpu()
