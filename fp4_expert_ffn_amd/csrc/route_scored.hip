@@ -393,7 +393,8 @@ __device__ __forceinline__ float route_row(const RouterP& R, const float* __rest
     live = live && maybe < R.topk_group;
     // rows whose groups are open (a NaN among the keys leaves the ranks above
     // without meaning): their groups in 64 bits
-    const uint64_t open = __ballot(group < R.n_group && (nan || (maybe >= R.topk_group && above < R.topk_group)));
+    const uint64_t open =
+        __ballot(valid && group < R.n_group && (nan || (maybe >= R.topk_group && above < R.topk_group)));
     if (open != 0ull) {
       const uint64_t row_mask = (LR == 64 ? ~0ull : (1ull << (LR & 63)) - 1ull) << (lane - p);
       double den64 = 1.0;
@@ -450,7 +451,7 @@ __device__ __forceinline__ float route_row(const RouterP& R, const float* __rest
     const uint32_t mx = row_max_u32<LR>(w[0]);
     const float v = unrank32(mx & ~(uint32_t)(NPL - 1));
     const bool close = r > 0 && !(last - v > s_err + kCut * fmaxf(fabsf(last), fabsf(v)));
-    if (r >= k && (mx == 0u || !close)) n = min(n, r);
+    if (r >= k && (mx == 0u || !close || !valid)) n = min(n, r);  // (a row past the batch is all ties)
     if (r >= k && __ballot(n > r) == 0ull) break;  // every row of the wave ends here
     if (r == kRouteMaxK) break;
     near = near || (close && r < n);
@@ -823,11 +824,13 @@ extern "C" moe_status moe_route_scored_permute(const moe_router* r, const float*
   // idle: routed by a launch of its own over all CUs, then permuted.  Before
   // and after (us, k = 8): 64 tokens of 512 experts 27 -> 15, 1000 of 3 x 160
   // 63 -> 21, of 200 experts (one pass) 16 -> 15, 4000 of 320 (4 passes) 33 ->
-  // 31; 4000 of 8 x 32 (one pass) 22 -> 24, 16384 of 512 41 -> 87.
+  // 31; 4000 of 8 x 32 (one pass) 22 -> 24, 16384 of 512 41 -> 87.  A second
+  // pass over short rows without groups costs less than a launch: 64 tokens
+  // of 128 11.4 -> 12.1.
   int passes = 1;
   with_shape(R, E, T <= 16, [&](auto lr, auto npl) {
     const int rows = kMaxThreads<decltype(lr)::value, decltype(npl)::value> / decltype(lr)::value;
-    passes = (std::min(T, T <= kChunk ? kChunk : C) + rows - 1) / rows;
+    if (decltype(npl)::value > 8 || R.n_group > 1) passes = (std::min(T, T <= kChunk ? kChunk : C) + rows - 1) / rows;
   });
   // or nothing to route, or more experts than a chunk's part of inv has words for their counts
   if (T == 0 || (T > kChunk && E > kChunk * k) || (passes > 1 && T <= 1024 * passes)) {
