@@ -133,13 +133,33 @@ void launch_small(const LinParams& P, hipStream_t s) {
   else launch_small_gate<QM, false>(P, s);
 }
 
+// Whether k_linear_small takes the call.  It is bound by what one CU can load
+// (every workgroup reads its 16 or 32 whole weight rows and all of x), the
+// tile kernel with its split K by launches and HBM.  The estimates in us, fit
+// to 1 to 17 tokens of 256 to 7168 rows of 2 to 14 KB: few-token form 2 + a
+// workgroup's KB (weights 0.032, x 0.02) a turn, tiles 7.3 + bytes at 8 TB/s.
+// One token, bf16: 4096 x 4096 8.3 against 11.8, 128 + 128 gated rows of 7168
+// 16.3 against 8.8; 16 tokens: 7168 x 2048 10.4 against 10.6, 7168 x 7168 27.3
+// against 20.1.  Decoded E4M3 (fp32 outputs) costs the tiles more: 2048 x 2048
+// 4.0 against 12.9, 7168 x 7168 15.8 against 15.7.
+bool small_wins(int T, int R, bool gated, int kb, bool exact) {
+  if (T > kSmallMaxT) return false;
+  if (exact) return true;
+  const float row = (float)kb * 1e-3f;
+  const int turns = ((gated ? R / 2 : R) + 16 * 256 - 1) / (16 * 256);
+  const float few = 2.f + row * ((gated ? 32 : 16) * 0.032f + (float)T * 0.02f) * (float)turns;
+  return few <= 7.3f + (float)R * (float)kb * 1.25e-7f;
+}
+
 }  // namespace
 
 extern "C" size_t moe_linear_workspace_size(const moe_linear_args* a) {
-  if (!a || a->T <= kSmallMaxT || a->N < 1 || a->K < 1 || a->T >= (1 << 24) || a->N >= (1 << 24) || a->K >= (1 << 24))
+  if (!a || a->T < 1 || a->N < 1 || a->K < 1 || a->T >= (1 << 24) || a->N >= (1 << 24) || a->K >= (1 << 24))
     return 0;
   const int kb = a->K * (a->qmode == MOE_Q_NONE ? 2 : 1);
-  return linear_tile_workspace(a->T, a->gated ? 2 * a->N : a->N, kb, a->qmode != MOE_Q_NONE && a->out_f32);
+  const int R = a->gated ? 2 * a->N : a->N;
+  const bool exact = a->qmode != MOE_Q_NONE && a->out_f32;
+  return small_wins(a->T, R, a->gated, kb, exact) ? 0 : linear_tile_workspace(a->T, R, kb, exact);
 }
 
 extern "C" moe_status moe_linear(const moe_linear_args* a, moe_stream_t stream) {
@@ -186,7 +206,8 @@ extern "C" moe_status moe_linear(const moe_linear_args* a, moe_stream_t stream) 
   P.fn = a->fn;
   P.gated = a->gated;
   P.out_f32 = a->out_f32;
-  const bool tile = a->T > kSmallMaxT && linear_tile_fits(P);
+  const bool tile =
+      !small_wins(P.T, P.R, P.gated, P.kb, a->qmode != MOE_Q_NONE && P.out_f32) && linear_tile_fits(P);
   const size_t need = tile ? moe_linear_workspace_size(a) : 0;
   if (need > 0) {
     if (!a->workspace || a->workspace_bytes < need)

@@ -124,6 +124,22 @@ SMALL = [(1, 16, 128), (1, 1, 128), (2, 17, 256), (16, 64, 384), (15, 33, 1024),
          (1, 256, 7168)]
 
 
+# few tokens whose rows are too long for one CU to stream: the tiles, K split
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,N,K,fmt,gated", [
+    (1, 40, 8192, "bf16", True), (1, 33, 15000, "bf16", False), (16, 70, 7168, "bf16", False),
+    (2, 64, 14336, "fp8", True), (16, 100, 16000, "fp8", False), (13, 72, 8192, "mxfp8", True),
+    (16, 4112, 7168, "bf16", False)])
+def test_linear_few_tokens_long_rows(m, T, N, K, fmt, gated):
+    need_gpu()
+    n = m.moe_linear_workspace_size(_ok(m, T=T, N=N, K=K, fmt=fmt, gated=gated))
+    assert n > 0  # split
+    for strided in (False, True):
+        run_case(m, T, N, K, fmt, fn="silu" if gated else "none", gated=gated, bias=True, res=strided, strided=strided)
+    # fp32 outputs of 8-bit operands: the few-token form at any length
+    run_case(m, T, N, K, fmt, gated=gated, out="f32")
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("fmt", ["bf16", "fp8", "mxfp8"])
 @pytest.mark.parametrize("T,N,K", SMALL)
