@@ -13,27 +13,33 @@ namespace {
 
 using namespace moe;
 
-// Few tokens: a stream of the weights.  One workgroup: 16 columns (gated:
+// Few tokens: a stream of the weights.  One workgroup: NC columns (gated:
 // their gate and up rows) x 16 tokens; its NWV waves take runs of kU K-steps
-// in turn and load a run at once (gated: 16 KiB of weights a wave in flight),
-// so that a row of up to NWV * kU steps costs one memory latency; the waves'
-// sums are joined in LDS in wave order.
+// in turn and load a run at once (gated, 16 columns: 16 KiB of weights a wave
+// in flight), so that a row of up to NWV * kU steps costs one memory latency;
+// the waves' sums are joined in LDS in wave order.  NC = 8 (gated): the gate
+// and up rows of 8 columns are the rows of one fragment, twice the workgroups
+// where 16 columns leave CUs idle (one token, 2048 + 2048 FP8 rows of 7168:
+// 9.1 -> 6.6 us, 4.5 TB/s; 3584 + 3584 rows fill the chip with 16 columns).
+// Bound: what a CU can load (few workgroups), else HBM.
 constexpr int kSmallMaxT = 16;  // longer batches: the tile kernel
 constexpr int kU = 4;
 
-template <int QM, bool GATED, bool EXACT, int NWV>
+template <int QM, bool GATED, bool EXACT, int NC, int NWV>
 __global__ __launch_bounds__(64 * NWV) void k_linear_small(LinParams P, int n_tiles) {
-  constexpr int NB = GATED ? 2 : 1;
+  static_assert(NC == 16 || (NC == 8 && GATED), "whole fragments");
+  constexpr int NB = GATED && NC == 16 ? 2 : 1;
   constexpr bool MX = QM == MOE_Q_MXFP8;
   __shared__ float part[NWV][NB][256];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int n0 = (int)(blockIdx.x % n_tiles) * 16, t0 = (int)(blockIdx.x / n_tiles) * 16;
+  const int n0 = (int)(blockIdx.x % n_tiles) * NC, t0 = (int)(blockIdx.x / n_tiles) * 16;
   const int r = lane & 15, g = lane >> 4;
-  const int t = min(t0 + r, P.T - 1), n = min(n0 + r, P.N - 1);  // rows past the end re-read the last one
+  // rows past the end re-read the last one
+  const int t = min(t0 + r, P.T - 1), n = min(n0 + r % NC, P.N - 1) + (r >= NC ? P.N : 0);
   const uint8_t* xp = P.x + (int64_t)t * P.ldx;
   const uint8_t* wp[NB];
   wp[0] = P.w + (int64_t)n * P.ldw;
-  if (GATED) wp[1] = P.w + (int64_t)(P.N + n) * P.ldw;
+  if constexpr (NB == 2) wp[1] = P.w + (int64_t)(P.N + n) * P.ldw;
   lf32x4_t acc[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) acc[b] = lf32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -92,39 +98,55 @@ __global__ __launch_bounds__(64 * NWV) void k_linear_small(LinParams P, int n_ti
   }
 #pragma unroll
   for (int b = 0; b < NB; ++b) *reinterpret_cast<lf32x4_t*>(&part[wave][b][lane * 4]) = acc[b];
-  // thread o: token o / 16, column o % 16; what its epilogue reads is loaded ahead of the barrier
-  for (int o = tid; o < 256; o += 64 * NWV) {
-    const int to = t0 + o / 16, c = n0 + o % 16;
-    const bool mine = to < P.T && c < P.N;
-    Epilogue<QM, GATED> e;
-    if (mine) e.load(P, to, c);
-    if (o == tid) __syncthreads();
-    if (!mine) continue;
-    const int at = (o / 16 + 16 * ((o % 16) >> 2)) * 4 + (o & 3);
-    float a = 0.f, u = 0.f;
+  // thread o: token o / NC, column o % NC; what its epilogue reads is loaded ahead of the barrier
+  static_assert(64 * NWV >= 256, "an output a thread at most");
+  const int tl = tid / NC, cl = tid % NC, to = t0 + tl, c = n0 + cl;
+  const bool mine = tl < 16 && to < P.T && c < P.N;
+  Epilogue<QM, GATED> e;
+  if (mine) e.load(P, to, c);
+  __syncthreads();
+  if (!mine) return;
+  const int at = (tl + 16 * (cl >> 2)) * 4 + (cl & 3);
+  float a = 0.f, u = 0.f;
 #pragma unroll
-    for (int i = 0; i < NWV; ++i) {
-      a += part[i][0][at];
-      if (GATED) u += part[i][NB - 1][at];
-    }
-    put(P, to, c, e.finish(P, a, u));
+  for (int i = 0; i < NWV; ++i) {
+    a += part[i][0][at];
+    if (GATED) u += NB == 2 ? part[i][NB - 1][at] : part[i][0][at + 16 * (NC / 4) * 4];  // up: rows NC .. of the fragment
   }
+  put(P, to, c, e.finish(P, a, u));
+}
+
+// us of a call by what a CU loads: 2 + a workgroup's KB (weights 0.032, x
+// 0.02) for each workgroup in turn; rows: weight rows a workgroup.
+float few_cost(int T, int N, int kb, int cols, int rows) {
+  const int turns = (N + cols * 256 - 1) / (cols * 256);
+  return 2.f + (float)kb * 1e-3f * ((float)rows * 0.032f + (float)T * 0.02f) * (float)turns;
+}
+
+bool eight_columns(int T, int N, int kb) { return few_cost(T, N, kb, 8, 16) < few_cost(T, N, kb, 16, 32); }
+
+template <int QM, bool GATED, bool EXACT, int NC>
+void launch_small_waves(const LinParams& P, hipStream_t s) {
+  const int nt = (P.N + NC - 1) / NC, tt = (P.T + 15) / 16;
+  const dim3 g((unsigned)((long long)nt * tt));
+  const int steps = (P.kb + 127) / 128;
+  if (steps > 8 * kU) launch(k_linear_small<QM, GATED, EXACT, NC, 16>, g, dim3(1024), 0, s, P, nt);
+  else if (steps > 4 * kU) launch(k_linear_small<QM, GATED, EXACT, NC, 8>, g, dim3(512), 0, s, P, nt);
+  else launch(k_linear_small<QM, GATED, EXACT, NC, 4>, g, dim3(256), 0, s, P, nt);
 }
 
 template <int QM, bool GATED, bool EXACT>
-void launch_small_waves(const LinParams& P, hipStream_t s) {
-  const int nt = (P.N + 15) / 16, tt = (P.T + 15) / 16;
-  const dim3 g((unsigned)((long long)nt * tt));
-  const int steps = (P.kb + 127) / 128;
-  if (steps > 8 * kU) launch(k_linear_small<QM, GATED, EXACT, 16>, g, dim3(1024), 0, s, P, nt);
-  else if (steps > 4 * kU) launch(k_linear_small<QM, GATED, EXACT, 8>, g, dim3(512), 0, s, P, nt);
-  else launch(k_linear_small<QM, GATED, EXACT, 4>, g, dim3(256), 0, s, P, nt);
+void launch_small_cols(const LinParams& P, hipStream_t s) {
+  if constexpr (GATED) {
+    if (eight_columns(std::min(P.T, 16), P.N, P.kb)) return launch_small_waves<QM, GATED, EXACT, 8>(P, s);
+  }
+  launch_small_waves<QM, GATED, EXACT, 16>(P, s);
 }
 
 template <int QM, bool GATED>
 void launch_small_gate(const LinParams& P, hipStream_t s) {
-  if (QM != MOE_Q_NONE && P.out_f32) launch_small_waves<QM, GATED, QM != MOE_Q_NONE>(P, s);
-  else launch_small_waves<QM, GATED, false>(P, s);
+  if (QM != MOE_Q_NONE && P.out_f32) launch_small_cols<QM, GATED, QM != MOE_Q_NONE>(P, s);
+  else launch_small_cols<QM, GATED, false>(P, s);
 }
 
 template <int QM>
@@ -134,20 +156,18 @@ void launch_small(const LinParams& P, hipStream_t s) {
 }
 
 // Whether k_linear_small takes the call.  It is bound by what one CU can load
-// (every workgroup reads its 16 or 32 whole weight rows and all of x), the
-// tile kernel with its split K by launches and HBM.  The estimates in us, fit
-// to 1 to 17 tokens of 256 to 7168 rows of 2 to 14 KB: few-token form 2 + a
-// workgroup's KB (weights 0.032, x 0.02) a turn, tiles 7.3 + bytes at 8 TB/s.
-// One token, bf16: 4096 x 4096 8.3 against 11.8, 128 + 128 gated rows of 7168
-// 16.3 against 8.8; 16 tokens: 7168 x 2048 10.4 against 10.6, 7168 x 7168 27.3
-// against 20.1.  Decoded E4M3 (fp32 outputs) costs the tiles more: 2048 x 2048
-// 4.0 against 12.9, 7168 x 7168 15.8 against 15.7.
+// (every workgroup reads its whole weight rows and all of x), the tile kernel
+// with its split K by launches and HBM: about 7.3 us + bytes at 8 TB/s.  Both
+// estimates are fit to 1 to 17 tokens of 256 to 7168 rows of 2 to 14 KB.  One
+// token, bf16: 4096 x 4096 8.3 against 11.8 us; 16 tokens: 7168 x 2048 10.4
+// against 10.6, 7168 x 7168 27.3 against 20.1.  Decoded E4M3 (fp32 outputs)
+// costs the tiles more: 2048 x 2048 4.0 against 12.9, 7168 x 7168 15.8 against
+// 15.7.
 bool small_wins(int T, int R, bool gated, int kb, bool exact) {
   if (T > kSmallMaxT) return false;
   if (exact) return true;
-  const float row = (float)kb * 1e-3f;
-  const int turns = ((gated ? R / 2 : R) + 16 * 256 - 1) / (16 * 256);
-  const float few = 2.f + row * ((gated ? 32 : 16) * 0.032f + (float)T * 0.02f) * (float)turns;
+  const float few = gated ? std::min(few_cost(T, R / 2, kb, 8, 16), few_cost(T, R / 2, kb, 16, 32))
+                          : few_cost(T, R, kb, 16, 16);
   return few <= 7.3f + (float)R * (float)kb * 1.25e-7f;
 }
 
