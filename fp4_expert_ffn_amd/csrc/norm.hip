@@ -8,7 +8,10 @@
 // needs no second reduction: |y| = |r w| * rstd, and multiplying by rstd
 // keeps the order after rounding, so max |y| = max |r w| * rstd; the sum of
 // squares and max |r w| are reduced together.
-// Bound: HBM (a few flops a byte); with few rows, one memory latency.
+// Bound: HBM (a few flops a byte); with few rows, one memory latency.  16384
+// x 7168, bf16 residual in and out, MXFP8 out (826 MB): 141 us, 5.9 TB/s; a
+// copy of 1 GiB reaches 5.0.  1027 x 2048, fp32 residual, FP8 and bf16 out (27
+// MB): 6.4 us.  One row of 7168: 2.3 us, one of 64 2.1.
 #include <algorithm>
 
 #include "common.h"
@@ -84,7 +87,7 @@ __device__ __forceinline__ float wave_fmax(float v) {
 // TPR threads a row (64: four rows a workgroup), NV chunks of 8 TPR columns.
 // NORM false: the encoding of x alone.
 template <int TPR, int NV, int RES, int QM, bool NORM>
-__global__ __launch_bounds__(TPR == 1024 ? 1024 : 256) void k_norm(NormParams P) {
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm(NormParams P) {
   constexpr int RPW = TPR == 64 ? 4 : 1;
   constexpr int WPR = TPR / 64;  // waves a row
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -229,19 +232,27 @@ __global__ __launch_bounds__(TPR == 1024 ? 1024 : 256) void k_norm(NormParams P)
 
 template <int RES, int QM, bool NORM>
 void launch_norm(const NormParams& P, hipStream_t s) {
+  // Few values a thread, so that a CU holds many rows' loads; a wave a row
+  // only where a wider row would leave most of its threads idle.  8000 rows,
+  // bf16 and MXFP8 out, us: H = 1024 64 x 2 chunks 11.2 and 11.8, 256 x 1 12.7
+  // and 13.8; 2048 256 x 1 21.7 and 19.9, 64 x 4 21.9 and 22.2 (one row 2.1
+  // and 2.4 against 2.9 and 3.7); 4096 256 x 2 46.7 and 44.3, 512 x 1 47.9 and
+  // 45.0; 8192 512 x 2 90.4 and 83.1, 256 x 4 98.4 and 91.5, 1024 x 1 94.2 and
+  // 85.7; 16384 1024 x 2 192 and 165, 512 x 4 194 and 172, 1024 x 4 189 and
+  // 188 (one row 3.3 against 3.9).
   const int chunks = (P.H + 7) / 8;
-  if (chunks <= 256) {
+  if (chunks <= 128) {
     const dim3 g((unsigned)((P.T + 3) / 4));
     if (chunks <= 64) launch(k_norm<64, 1, RES, QM, NORM>, g, dim3(256), 0, s, P);
-    else if (chunks <= 128) launch(k_norm<64, 2, RES, QM, NORM>, g, dim3(256), 0, s, P);
-    else launch(k_norm<64, 4, RES, QM, NORM>, g, dim3(256), 0, s, P);
-  } else if (chunks <= 1024) {
-    const dim3 g((unsigned)P.T);
-    if (chunks <= 512) launch(k_norm<256, 2, RES, QM, NORM>, g, dim3(256), 0, s, P);
-    else launch(k_norm<256, 4, RES, QM, NORM>, g, dim3(256), 0, s, P);
-  } else {
-    launch(k_norm<1024, 4, RES, QM, NORM>, dim3((unsigned)P.T), dim3(1024), 0, s, P);
+    else launch(k_norm<64, 2, RES, QM, NORM>, g, dim3(256), 0, s, P);
+    return;
   }
+  const dim3 g((unsigned)P.T);
+  if (chunks <= 256) launch(k_norm<256, 1, RES, QM, NORM>, g, dim3(256), 0, s, P);
+  else if (chunks <= 512) launch(k_norm<256, 2, RES, QM, NORM>, g, dim3(256), 0, s, P);
+  else if (chunks <= 1024) launch(k_norm<512, 2, RES, QM, NORM>, g, dim3(512), 0, s, P);
+  else if (chunks <= 2048) launch(k_norm<1024, 2, RES, QM, NORM>, g, dim3(1024), 0, s, P);
+  else launch(k_norm<1024, 4, RES, QM, NORM>, g, dim3(1024), 0, s, P);
 }
 
 template <int RES>

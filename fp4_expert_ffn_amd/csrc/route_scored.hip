@@ -17,8 +17,11 @@
 // lane.  A lane sorts its keys once (a Batcher network on 32-bit words that
 // carry the expert's place in the lane in their last bits), so a round of the
 // top-k is a maximum over the lanes' first words (DPP) and a shift in the lane
-// that had it.  Bound: VALU issue (about 130 instructions a row at 256
-// experts; the logits' bytes need less), one memory latency for few rows.
+// that had it.  Bound: VALU issue and the latency of dependent cross-lane
+// steps (the logits' bytes need a tenth of the time), for few rows a chain of
+// one memory latency, the rounds and the scan.  Kernel times at 256 experts
+// in 8 groups, k = 8: one token 7.0 us; 16384 tokens 24 us for the rows, 3 + 3
+// for the permutation; 4099 tokens of 128 experts without groups 8.5 + 3 + 3.
 #include <algorithm>
 #include <type_traits>
 

@@ -111,6 +111,16 @@ def test_norm_matches_the_formula(m, T, H, res, weight, out, q):
         assert torch.all(qd[:, H:] == 0x55)
 
 
+# Widths on both sides of where a row takes more threads.
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,q", [(9, 1032, "fp8"), (9, 1152, "mxfp8"), (5, 2048, "none"), (5, 2176, "mxfp8"),
+                                   (5, 4104, "fp8"), (3, 4224, "mxfp8"), (3, 8192, "mxfp8"), (3, 8320, "mxfp8"),
+                                   (2, 16384, "mxfp8"), (2, 16384, "fp8"), (2, 16392, "fp8"), (2, 16512, "mxfp8")])
+def test_norm_row_widths(m, T, H, q):
+    test_norm_matches_the_formula(m, T, H, "bf16", "f32", True, q)
+    test_norm_matches_the_formula(m, T, H, "f32", "bf16", True, q)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("res", ["bf16", "f32"])
 def test_norm_in_place(m, res):
