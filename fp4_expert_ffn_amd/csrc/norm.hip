@@ -262,14 +262,16 @@ void launch_norm_q(const NormParams& P, int qm, hipStream_t s) {
   else launch_norm<RES, MOE_Q_MXFP8, true>(P, s);
 }
 
+constexpr int kMaxRows = 1 << 22;  // x 1024 threads: what a grid holds (below 2^32 threads)
+
 bool misaligned(const void* p, unsigned a) { return ((uintptr_t)p & (a - 1)) != 0; }
 
 }  // namespace
 
 extern "C" moe_status moe_rmsnorm(const moe_norm_args* a, moe_stream_t stream) {
   MOE_CHECK_ARG(a, "moe_rmsnorm: null pointer");
-  MOE_CHECK_ARG(a->T >= 0 && a->H >= 8 && a->H <= 32768 && a->H % 8 == 0,
-                "moe_rmsnorm: bad sizes T=%d H=%d (H a multiple of 8, at most 32768)", a->T, a->H);
+  MOE_CHECK_ARG(a->T >= 0 && a->T < kMaxRows && a->H >= 8 && a->H <= 32768 && a->H % 8 == 0,
+                "moe_rmsnorm: bad sizes T=%d H=%d (T below 2^22, H a multiple of 8, at most 32768)", a->T, a->H);
   MOE_CHECK_ARG(a->eps >= 0.f, "moe_rmsnorm: eps must be >= 0");
   MOE_CHECK_ARG(a->qmode >= MOE_Q_NONE && a->qmode <= MOE_Q_MXFP8, "moe_rmsnorm: bad qmode %d", a->qmode);
   MOE_CHECK_ARG(a->qmode != MOE_Q_MXFP8 || a->H % 128 == 0, "moe_rmsnorm: MXFP8 rows need H %% 128 == 0, H=%d", a->H);
@@ -298,8 +300,9 @@ extern "C" moe_status moe_rmsnorm(const moe_norm_args* a, moe_stream_t stream) {
 
 extern "C" moe_status moe_quantize_fp8(const uint16_t* x, int64_t ldx, int rows, int cols, int qmode, uint8_t* q,
                                        void* q_scale, moe_stream_t stream) {
-  MOE_CHECK_ARG(rows >= 0 && cols >= 8 && cols <= 32768 && cols % 8 == 0,
-                "moe_quantize_fp8: bad sizes rows=%d cols=%d (cols a multiple of 8, at most 32768)", rows, cols);
+  MOE_CHECK_ARG(rows >= 0 && rows < kMaxRows && cols >= 8 && cols <= 32768 && cols % 8 == 0,
+                "moe_quantize_fp8: bad sizes rows=%d cols=%d (rows below 2^22, cols a multiple of 8, at most 32768)",
+                rows, cols);
   MOE_CHECK_ARG(qmode == MOE_Q_FP8 || qmode == MOE_Q_MXFP8, "moe_quantize_fp8: bad qmode %d", qmode);
   MOE_CHECK_ARG(qmode != MOE_Q_MXFP8 || cols % 128 == 0, "moe_quantize_fp8: MXFP8 rows need cols %% 128 == 0, cols=%d",
                 cols);

@@ -729,7 +729,9 @@ __global__ __launch_bounds__(512) void k_chunk_place(const int32_t* __restrict__
 
 moe_status check_router(const char* who, const moe_router* r, int T, int E, int k) {
   MOE_CHECK_ARG(r, "%s: null router", who);
-  MOE_CHECK_ARG(T >= 0 && E >= 1 && E <= 1024, "%s: bad sizes T=%d E=%d (E <= 1024)", who, T, E);
+  // T: four rows a workgroup of 256 threads at least, in a grid below 2^32 threads
+  MOE_CHECK_ARG(T >= 0 && T < (1 << 25) && E >= 1 && E <= 1024, "%s: bad sizes T=%d E=%d (T < 2^25, E <= 1024)", who, T,
+                E);
   MOE_CHECK_ARG(r->score == MOE_SCORE_SOFTMAX || r->score == MOE_SCORE_SIGMOID, "%s: bad score %d", who, r->score);
   MOE_CHECK_ARG(r->group_rank == MOE_GROUP_MAX || r->group_rank == MOE_GROUP_TOP2, "%s: bad group_rank %d", who,
                 r->group_rank);

@@ -133,7 +133,8 @@ typedef struct {
  * The weights: w_j = s_j (NaN logits: 0; -inf logits under sigmoid: 0), with
  * renormalize divided by their sum over the k selected; a row whose weights
  * would all be 0 by a zero sum gets 1/k each; all times scale.
- * Requires 1 <= k <= min(topk_group * (E / n_group), 16), E <= 1024, T >= 0. */
+ * Requires 1 <= k <= min(topk_group * (E / n_group), 16), E <= 1024,
+ * 0 <= T < 2^25. */
 moe_status moe_route_scored(const moe_router* r, const float* logits, int T, int E, int k, int32_t* topk_ids,
                             float* topk_w, moe_stream_t stream);
 
@@ -324,7 +325,7 @@ typedef enum { MOE_Q_NONE = 0, MOE_Q_FP8 = 1, MOE_Q_MXFP8 = 2 } moe_qmode;
  * 8).  Rows of H elements; what lies between a row's end and the next row's
  * start is neither read nor written. */
 typedef struct {
-  int T, H;                 /* tokens, hidden; H % 8 == 0, 8 <= H <= 32768           */
+  int T, H;                 /* tokens, hidden; T < 2^22, H % 8 == 0, 8 <= H <= 32768 */
   const uint16_t* x;        /* [T,H] bf16                                            */
   int64_t ldx;
   const void* weight;       /* nullable (1): [H] bf16, or fp32 with weight_f32       */
@@ -358,7 +359,7 @@ moe_status moe_rmsnorm(const moe_norm_args* a, moe_stream_t stream);
 /* The 8-bit encoding alone: q, q_scale of the bf16 rows x [rows, cols]
  * (row stride ldx, 0 for cols; q dense), by moe_rmsnorm's kernel without the
  * norm: the operand of a moe_linear whose input is another product's output.
- * cols as H above. */
+ * rows and cols as T and H above. */
 moe_status moe_quantize_fp8(const uint16_t* x, int64_t ldx, int rows, int cols, int qmode, uint8_t* q, void* q_scale,
                             moe_stream_t stream);
 

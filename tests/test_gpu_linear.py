@@ -268,6 +268,37 @@ def test_fp8_instruction_cuts_small_products(m):
         assert torch.all((o.cpu().float() - 2 * small[:, None]).abs() <= off)
 
 
+@pytest.mark.gpu
+def test_linear_few_tokens_captured(m):
+    """A split product of few tokens, replayed with new inputs and a workspace filled in between."""
+    need_gpu()
+    T, N, K = 3, 80, 8192
+    x, w = torch.zeros((T, K), dtype=torch.bfloat16, device=DEV), _rand(1, N, K).to(torch.bfloat16).to(DEV)
+    outs = [torch.empty((T, N), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    args = []
+    for o in outs:
+        a = m.linear_args(x=x, w=w, out=o)
+        n = m.moe_linear_workspace_size(a)
+        assert n > 0
+        a.buf = torch.empty(n, dtype=torch.uint8, device=DEV)
+        a.workspace, a.workspace_bytes = a.buf.data_ptr(), n
+        args.append(a)
+    say("captured split product of few tokens")
+    m.moe_linear(args[0])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        m.moe_linear(args[0])
+    for seed in range(3):
+        x.copy_(_rand(20 + seed, T, K).to(torch.bfloat16))
+        m.moe_linear(args[1])
+        for fill in (0xFF, 0x00):
+            args[0].buf.fill_(fill)
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(outs[0], outs[1])
+
+
 def _ok(L, **kw):
     a = dict(T=4, N=32, K=128, x=0x10000, w=0x20000, out=0x30000)
     a.update(kw)

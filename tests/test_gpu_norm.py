@@ -273,3 +273,13 @@ def test_quantize_fp8_refusals(m, args, msg):
     with pytest.raises(m.MoeError) as e:
         m.moe_quantize_fp8(x, rows, cols, qm, q, s, stream=0, ldx=ldx)
     assert e.value.status == 1 and msg in str(e.value)
+
+
+def test_norm_refuses_more_rows_than_a_grid_holds(m):
+    for n in (1 << 22, (1 << 31) - 1):
+        with pytest.raises(m.MoeError) as e:
+            m.moe_rmsnorm(m.norm_args(x=0x10000, T=n, H=64, out=0x20000), stream=0)
+        assert e.value.status == 1 and "bad sizes" in str(e.value)
+        with pytest.raises(m.MoeError) as e:
+            m.moe_quantize_fp8(0x10000, n, 64, "fp8", 0x20000, 0x30000, stream=0)
+        assert e.value.status == 1 and "bad sizes" in str(e.value)

@@ -279,6 +279,39 @@ def test_route_refuses_nulls_and_bad_biases(m):
             m.router(bias=bias)
 
 
+def test_route_refuses_more_rows_than_a_grid_holds(m):
+    for T in (1 << 25, (1 << 31) - 1):
+        with pytest.raises(m.MoeError) as e:
+            m.moe_route_scored(m.router(), 0x10000, T, 8, 2, 0x20000, 0x30000, stream=0)
+        assert e.value.status == 1 and "bad sizes" in str(e.value)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,G", [(64, 512, 1), (1, 210, 3), (300, 480, 8), (300, 128, 1)])
+def test_route_captured(m, T, E, G):
+    """Replays with new logits give the eager results, whatever launches the batch takes."""
+    need_gpu()
+    k = 8
+    i32 = lambda *n: torch.empty(n, dtype=torch.int32, device=DEV)  # noqa: E731
+    new = lambda: (i32(T, k), torch.empty((T, k), device=DEV), i32(E), i32(E + 1), i32(T * k), i32(T * k))  # noqa: E731
+    r = m.router(score="softmax", n_group=G, topk_group=max(1, G // 2), group_rank="top2")
+    lg = torch.zeros((T, E), device=DEV)
+    a, b = new(), new()
+    say(f"captured route T={T} E={E} G={G}")
+    m.moe_route_scored_permute(r, lg, T, E, k, *a)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        m.moe_route_scored_permute(r, lg, T, E, k, *a)
+    for seed in range(3):
+        lg.copy_(torch.from_numpy(np.random.default_rng(seed).standard_normal((T, E)).astype(np.float32)))
+        m.moe_route_scored_permute(r, lg, T, E, k, *b)
+        for _ in range(2):
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
 def test_route_refuses_tensors(m):
     """Strided, short or mistyped tensors and tensors outside the GPU never reach the kernels."""
     lg = torch.zeros(4, 64)
