@@ -35,9 +35,9 @@ namespace {
 using namespace moe;
 
 // Threads of a workgroup at most: 1024 (128 registers a lane) while a lane's
-// keys fit them, else 512 or 256.  No kernel here spills or
-// calls: a register saved where a branch has switched lanes off is lost to
-// them (a CPU test checks the compiled code).
+// keys fit them, else 512 or 256.  No kernel here spills
+// vector registers or calls: a register saved where a branch has switched
+// lanes off is lost to them (a CPU test checks the compiled code).
 template <int LR, int NPL>
 constexpr int kMaxThreads = NPL > 16 ? 256 : (NPL >= 8 ? 512 : 1024);
 
