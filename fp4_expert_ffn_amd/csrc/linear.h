@@ -80,12 +80,14 @@ __device__ __forceinline__ lf32x4_t mma_decoded(const Frag& w, const Frag& x, lf
 }
 
 // exp(z) by the hardware exp2 (1 ulp), the rounding of z log2(e) put back:
-// within 2 ulp over the whole range.
+// within 2 ulp where the result lies in the normal range.  From 2^128 on exp2
+// is infinite and nothing is put back: infinity and a correction below zero
+// would be NaN.
 __device__ __forceinline__ float exp_f32(float z) {
   const float hi = z * 1.44269502f;
   const float lo = fmaf(z, 1.44269502f, -hi) + z * 1.92596303e-8f;  // log2(e) = 1.44269502 + 1.92596303e-8
   const float e = __builtin_amdgcn_exp2f(hi);
-  return fabsf(hi) < 200.f ? fmaf(e, lo * 0.693147182f, e) : e;  // past the range: 0 or infinity
+  return fabsf(hi) < 128.f ? fmaf(e, lo * 0.693147182f, e) : e;  // past the range: 0 or infinity
 }
 
 // The activation in fp32.  GELU's two forms as z * sigmoid(2 u) and with
