@@ -437,11 +437,12 @@ __device__ __forceinline__ float route_row(const RouterP& R, const float* __rest
     }
   }
 
-  // words: the key's order with its last bits replaced by the place in the lane (the lower place the larger)
+  // words: the key's order with its last bits replaced by the place in the lane (the lower place the larger); a NaN
+  // key takes the lowest of them that is not 0, the word of no expert
   uint32_t w[NPL];
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
-    const uint32_t k1 = (rank32(key[i]) & ~(uint32_t)(NPL - 1)) | (uint32_t)(NPL - 1 - i);
+    const uint32_t k1 = (max(rank32(key[i]), (uint32_t)NPL) & ~(uint32_t)(NPL - 1)) | (uint32_t)(NPL - 1 - i);
     w[i] = i < have && live ? k1 : 0u;
   }
   sort_desc<NPL>(w);
