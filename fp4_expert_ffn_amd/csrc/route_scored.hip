@@ -380,9 +380,16 @@ __device__ __forceinline__ float route_row(const RouterP& R, const float* __rest
     const float rank = R.top2 && R.gs > 1 ? a + b : a;
     // its place: the groups that are larger, or equal and lower.  Logits
     // compare exactly; scores alone are off by 2^-17 of themselves at most
-    // (exp of a difference of up to 88).
+    // (exp of a difference of up to 88).  Two keys of opposite signs were each
+    // rounded at their own size, beside which their sum may be small: the
+    // row's largest such loss counts for all its groups.
     const bool exact = !R.top2 && !R.bias;
-    const float tol = 2.f * s_err + (R.bias ? 0x1p-19f : 0x1p-16f) * fabsf(rank) + 0x1p-100f;
+    float size = fabsf(rank);
+    if (R.bias && R.top2) {
+      const float lost = a > 0.f && b < 0.f && b > -INFINITY ? 2.f * fminf(a, -b) : 0.f;  // |a| + |b| - |a + b|
+      size += __uint_as_float(row_max_u32<LR>(__float_as_uint(lost)));
+    }
+    const float tol = 2.f * s_err + (R.bias ? 0x1p-19f : 0x1p-16f) * size + 0x1p-100f;
     int above = 0, maybe = 0;  // groups surely before this one, and possibly
     const int lanes = R.n_group << R.lgs, first = lane - p;
     for (int d = 1; d < R.n_group; ++d) {

@@ -1,5 +1,6 @@
 """Scored routing where its fast choice works at its limits, against the rule in
-64 bits: NaN keys at every place of a lane."""
+64 bits: NaN keys at every place of a lane, and groups whose two best keys
+cancel."""
 import itertools
 
 import numpy as np
@@ -34,3 +35,20 @@ def test_two_nan_keys_rank_by_id(m, gs, G, score):
         check(m, rows, gs - 1, score=score, n_group=G, topk_group=1, group_rank="max")
         check(m, rows, gs - 1, score=score, n_group=G, topk_group=1, group_rank="max",
               bias=np.zeros(E, np.float32))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("big", [100.0, 1e3, 1e4, 1e6])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G", [(16, 8), (64, 8), (128, 4)])
+def test_groups_whose_best_keys_cancel(m, E, G, score, big):
+    """A forced expert (bias +big) and none but banned ones (-big) beside it in every group: a group's rank is
+    the small difference of two large keys, and decides between groups whose scores are close."""
+    need_gpu()
+    T, gs = 1500, E // G
+    rng = np.random.default_rng(int(big) + E)
+    logits = (rng.standard_normal((T, 1)) + rng.standard_normal((T, E)) * (20.0 / big)).astype(np.float32)
+    bias = np.full(E, -big, np.float32)
+    bias[rng.integers(0, gs, G) + gs * np.arange(G)] = big
+    check(m, logits, 2, score=score, n_group=G, topk_group=2, group_rank="top2", bias=bias)
+    check(m, logits[:40], 2, score=score, n_group=G, topk_group=G - 1, group_rank="top2", bias=bias)
