@@ -159,7 +159,11 @@ class DenseLayer:
     norm writing the first product's and moe_quantize_fp8 the second's.
     Weights: gate_up [2 I, H] (the I gate rows, then the I up rows) and down
     [H, I], bf16 or E4M3 codes with their scales (fp32 [rows], or E8M0
-    [cols / 128, rows, 4])."""
+    [cols / 128, rows, 4]).  They may be replaced between calls.
+
+    Every call writes the layer's own buffers (residual, h, out, the 8-bit
+    rows, the workspace): one layer serves one stream at a time, and the next
+    call replaces what the last returned."""
 
     def __init__(self, *, H, I, fmt, max_tokens, norm_weight, gate_up, down, gate_up_scale=None, down_scale=None,
                  eps=1e-6, device="cuda"):
@@ -175,10 +179,9 @@ class DenseLayer:
             self.q = torch.empty(T * max(H, I), dtype=torch.uint8, device=dev)
             self.q_scale = torch.empty(T * max(H, I) if fmt == "mxfp8" else 4 * T, dtype=torch.uint8, device=dev)
         # one workspace for every batch up to max_tokens: a captured call keeps its address
-        self._products = {}
         self._ws = None
         need = 0
-        for a in self._linear(T):
+        for a in self._linear(self.residual):
             for a.T in range(1, T + 1):
                 need = max(need, L.moe_linear_workspace_size(a))
         self._ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
@@ -189,15 +192,15 @@ class DenseLayer:
              self.q_scale[:4 * T].view(torch.float32))
         return self.q[:T * n].view(T, n), s
 
-    def _linear(self, T):
-        """Arguments of the two products for T tokens; the second's residual is set by the call."""
-        quant = self.fmt != "bf16"
+    def _linear(self, residual):
+        """Arguments of the two products with the present weights, the second's sum on residual [T, H]."""
+        T, quant = residual.shape[0], self.fmt != "bf16"
         nq, ns = self._rows(T, self.H) if quant else (self.n[:T], None)
         hq, hs = self._rows(T, self.I) if quant else (self.h[:T], None)
         up = L.linear_args(x=nq, w=self.gate_up, fmt=self.fmt, x_scale=ns, w_scale=self.gate_up_scale, act="silu",
                            gated=True, out=self.h[:T])
         down = L.linear_args(x=hq, w=self.down, fmt=self.fmt, x_scale=hs, w_scale=self.down_scale,
-                             residual=self.residual[:T], out=self.out[:T])
+                             residual=residual, out=self.out[:T])
         if self._ws is not None:
             for a in (up, down):
                 a.workspace, a.workspace_bytes = self._ws.data_ptr(), self._ws.numel()
@@ -210,23 +213,18 @@ class DenseLayer:
         assert T <= self.max_tokens
         if T == 0:
             return self.out[:0]
-        if T not in self._products:
-            self._products[T] = self._linear(T)
-        up, down = self._products[T]
+        kept = x if residual is None else self.residual[:T]  # the sum that goes on
+        up, down = self._linear(kept)
         quant = self.fmt != "bf16"
         nq, ns = self._rows(T, self.H) if quant else (self.n[:T], None)
         norm = L.norm_args(x=x, weight=self.norm_weight, eps=self.eps, residual=residual,
-                           residual_out=None if residual is None else self.residual[:T],
+                           residual_out=None if residual is None else kept,
                            **({"q": nq, "q_scale": ns, "qmode": self.fmt} if quant else {"out": nq}))
         L.moe_rmsnorm(norm, stream)
         L.moe_linear(up, stream)
         if quant:
             hq, hs = self._rows(T, self.I)
             L.moe_quantize_fp8(self.h[:T], T, self.I, self.fmt, hq, hs, stream)
-        if residual is None:  # the sum is x itself
-            down.residual, down.ldr = norm.x, norm.ldx
-        else:
-            down.residual, down.ldr = self.residual.data_ptr(), self.H
         L.moe_linear(down, stream)
         return self.out[:T]
 
