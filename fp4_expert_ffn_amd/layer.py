@@ -148,6 +148,16 @@ class MoELayer:
         raise AttributeError(name)
 
 
+def _other_rows(t, buf):
+    """Whether rows t overlap the dense rows buf other than row on row, so that a kernel could write one
+    before another workgroup has read it."""
+    T, a, b = len(buf), t.data_ptr(), buf.data_ptr()
+    if a == b and (T == 1 or t.stride(0) == buf.stride(0)):
+        return False
+    size = t.element_size()
+    return a < b + buf.numel() * size and b < a + ((T - 1) * t.stride(0) + t.shape[-1]) * size
+
+
 class DenseLayer:
     """The dense layer that stands where a sparse one could: residual addition
     and RMS norm, then a SwiGLU FFN whose products run on moe_linear, its
@@ -163,7 +173,8 @@ class DenseLayer:
 
     Every call writes the layer's own buffers (residual, h, out, the 8-bit
     rows, the workspace): one layer serves one stream at a time, and the next
-    call replaces what the last returned."""
+    call replaces what the last returned.  x or residual may be such a buffer's
+    first rows, but not other rows of it."""
 
     def __init__(self, *, H, I, fmt, max_tokens, norm_weight, gate_up, down, gate_up_scale=None, down_scale=None,
                  eps=1e-6, device="cuda"):
@@ -214,6 +225,10 @@ class DenseLayer:
         if T == 0:
             return self.out[:0]
         kept = x if residual is None else self.residual[:T]  # the sum that goes on
+        for t, buf in ((x, self.out),) if residual is None else ((x, self.residual), (residual, self.residual)):
+            if _other_rows(t, buf[:T]):
+                raise L.MoeError(L.MOE_EINVAL, "DenseLayer.forward: an input lies across other rows of a buffer that "
+                                               "the call writes: copy it first")
         up, down = self._linear(kept)
         quant = self.fmt != "bf16"
         nq, ns = self._rows(T, self.H) if quant else (self.n[:T], None)

@@ -49,3 +49,37 @@ def test_replaced_weights_of_another_shape_are_refused():
     with pytest.raises(m.MoeError) as e:
         layer.forward(x)
     assert "shape" in str(e.value)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+def test_inputs_in_the_layers_own_buffers(fmt):
+    """The last output's first rows as the next input: as from a copy.  Other rows of it, or every second one,
+    which the second product would overwrite while it adds them, are refused."""
+    need_gpu()
+    import fp4_expert_ffn_amd as m
+    layer, _, _, _ = dense(fmt)
+    x = _rand(1, 200, layer.H).to(torch.bfloat16).to(DEV)
+    say("dense layer, inputs in its own buffers", fmt)
+    y = layer.forward(x)
+    want = layer.forward(y.clone()).clone()
+    y = layer.forward(x)
+    assert torch.equal(layer.forward(y), want)
+    y = layer.forward(x)
+    part = y[3:90].clone()
+    for rows in (y[3:90], y[::2]):
+        with pytest.raises(m.MoeError) as e:
+            layer.forward(rows)
+        assert e.value.status == 1 and "copy" in str(e.value)
+    want = layer.forward(part).clone()
+    y = layer.forward(x)
+    assert torch.equal(layer.forward(y[110:197].copy_(part)), want)  # behind the rows written: no overlap
+    # a residual stream of its own buffer's rows
+    res = _rand(2, 200, layer.H).to(torch.bfloat16).to(DEV)
+    layer.forward(x, res)
+    kept = layer.residual[:200].clone()
+    want = layer.forward(x, kept).clone()
+    layer.residual[:200].copy_(kept)
+    assert torch.equal(layer.forward(x, layer.residual[:200]), want)
+    for a, b in ((x[:50], layer.residual[1:51]), (layer.residual[1:51], res[:50])):
+        with pytest.raises(m.MoeError):
+            layer.forward(a, b)
