@@ -188,7 +188,7 @@ class DenseLayer:
             self.n = bf16(H)
         else:
             self.q = torch.empty(T * max(H, I), dtype=torch.uint8, device=dev)
-            self.q_scale = torch.empty(T * max(H, I) if fmt == "mxfp8" else 4 * T, dtype=torch.uint8, device=dev)
+            self.q_scale = torch.empty(T * max(H, I) // 32 if fmt == "mxfp8" else 4 * T, dtype=torch.uint8, device=dev)
         # one workspace for every batch up to max_tokens: a captured call keeps its address
         self._ws = None
         need = 0

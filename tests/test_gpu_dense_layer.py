@@ -83,3 +83,10 @@ def test_inputs_in_the_layers_own_buffers(fmt):
     for a, b in ((x[:50], layer.residual[1:51]), (layer.residual[1:51], res[:50])):
         with pytest.raises(m.MoeError):
             layer.forward(a, b)
+
+
+def test_scale_buffer_holds_the_scales_alone():
+    """One byte per 32 columns of the wider of the two operands (MXFP8), four a row (FP8)."""
+    need_gpu()
+    for fmt, size in (("mxfp8", 300 * 384 // 32), ("fp8", 300 * 4)):
+        assert dense(fmt)[0].q_scale.numel() == size
