@@ -561,7 +561,9 @@ class Cache:
         if not h:
             raise MoeError(MOE_EINVAL, moe_last_error())
         self.handle = h
-        self.num_slots = num_slots
+        self.num_slots, self.num_experts = num_slots, num_experts
+        self._device = slot_pool.device.index if getattr(slot_pool, "is_cuda", False) else None
+        self._routers = {}  # layer (-1: every layer) -> router: their biases stay alive with the cache
 
     def close(self):
         if self.handle:
@@ -615,12 +617,20 @@ def moe_cache_use_copy_engine(cache: Cache, on: bool):
 
 
 def moe_cache_use_router(cache: Cache, layer: int, r: Router | None):
-    """Steps of `layer` (-1: every layer) route by the scored router r (None: softmax top-k again)."""
+    """Steps of `layer` (-1: every layer) route by the scored router r (None: softmax top-k again).
+    The bias needs the cache's number of experts and its pool's device; the cache keeps it alive until
+    another router takes its place (steps still queued by then need it kept by the caller)."""
     if r is not None:
-        cache._routers = getattr(cache, "_routers", {})
-        cache._routers[layer] = r  # its bias stays alive with the cache
+        n, dev = getattr(r, "_experts", None), getattr(r, "_device", None)
+        if n is not None and n != cache.num_experts:
+            _bad(f"moe_cache_use_router: the router's bias has {n} experts, the cache {cache.num_experts}")
+        if dev is not None and cache._device is not None and dev != cache._device:
+            _bad(f"moe_cache_use_router: the router's bias is on cuda:{dev}, the cache's pool on cuda:{cache._device}")
     _check(lib().moe_cache_use_router(cache.handle, int(layer), None if r is None else ctypes.byref(r)),
            "moe_cache_use_router")
+    if layer == -1:
+        cache._routers.clear()
+    cache._routers[layer] = r
 
 
 def moe_cache_pin_resident(cache: Cache, layer, s0):
