@@ -594,6 +594,18 @@ static moe_status ensure_side(moe_cache* c) {
   return MOE_OK;
 }
 
+// Whether the layer's router, if it has one, can route T tokens to k experts
+// each: a step is refused before it changes anything.
+static moe_status check_router_step(const moe_cache* c, int layer, int T, int k, const char* who) {
+  const moe_router* r = c->router(layer);
+  if (!r || T == 0) return MOE_OK;
+  const int most = moe::router_most(*r, c->num_experts);
+  MOE_CHECK_ARG(k <= most, "%s: k=%d, but the router of layer %d gives a token %d experts at most", who, k, layer, most);
+  MOE_CHECK_ARG((long long)T * k <= moe::kScoredMaxRows, "%s: T*k = %lld exceeds the router's %d", who,
+                (long long)T * k, moe::kScoredMaxRows);
+  return MOE_OK;
+}
+
 // ------------------------------------------------------------ one decode step
 
 // A step that returns early after enqueueing its hits on the side stream
@@ -619,6 +631,8 @@ static moe_status decode_step(moe_cache* c, moe_cache_step* s, moe_hybrid* hy, m
   MOE_CHECK_ARG(s->layer >= 0 && s->layer < c->num_layers, "%s: layer %d out of range", who, s->layer);
   MOE_CHECK_ARG(T >= 0 && f.k >= 1 && f.k <= E, "%s: bad T=%d k=%d", who, T, f.k);
   if (T == 0) return MOE_OK;
+  moe_status st = check_router_step(c, s->layer, T, f.k, who);
+  if (st != MOE_OK) return st;
   MOE_CHECK_ARG(s->logits && s->topk_ids && s->host_counts && s->host_map && s->dev_map && s->host_blobs,
                 "%s: null step buffer", who);
   MOE_CHECK_ARG(f.y && f.out && f.topk_w && f.inv && f.counts && f.offsets && f.perm,
@@ -631,7 +645,7 @@ static moe_status decode_step(moe_cache* c, moe_cache_step* s, moe_hybrid* hy, m
                   "%s: bad hybrid policy or host buffers", who);
   hipStream_t ks = reinterpret_cast<hipStream_t>(compute_stream);
   hipStream_t cs = reinterpret_cast<hipStream_t>(copy_stream);
-  moe_status st = ensure_events(c);
+  st = ensure_events(c);
   if (st != MOE_OK) return st;
 
   // 1-2. routing, then the step's experts on the host (and, for host-run
@@ -906,13 +920,15 @@ extern "C" moe_status moe_cache_prefill_step(moe_cache* c, moe_cache_prefill* s,
                     f.perm,
                 "moe_cache_prefill_step: logits, topk_ids, dev_map and ffn.out, topk_w, inv, counts, offsets, perm "
                 "are required");
+  moe_status st = check_router_step(c, s->layer, T, f.k, "moe_cache_prefill_step");
+  if (st != MOE_OK) return st;
   // every expert of the layer must be cached (its prefetch came first);
   // checked before any state changes
   for (int e = 0; e < E; ++e)
     if (c->key_slot[(size_t)s->layer * E + e] < 0)
       return moe::set_error(MOE_ECACHE, "moe_cache_prefill_step: expert (%d, %d) is not cached: prefetch the layer "
                             "first", s->layer, e);
-  moe_status st = ensure_events(c);
+  st = ensure_events(c);
   if (st != MOE_OK) return st;
   hipStream_t ks = reinterpret_cast<hipStream_t>(compute_stream);
   c->step_ids.resize(E);

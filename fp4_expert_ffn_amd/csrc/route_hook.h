@@ -2,9 +2,17 @@
 // by a router of their own.  The cache calls it through a pointer, so that its
 // host code links without the kernels.
 #pragma once
+#include <algorithm>
+
 #include "host_common.h"
 
 namespace moe {
+
+constexpr int kScoredMaxK = 16;              // experts a token
+constexpr int kScoredMaxRows = 1 << 17;      // tokens x experts a token of a permutation
+
+// The most experts a token can be given by *r (checked) over E: those of the groups it may take.
+inline int router_most(const moe_router& r, int E) { return std::min(r.topk_group * (E / r.n_group), kScoredMaxK); }
 
 // moe_route_scored_permute; with host_counts set, the counts copied there
 // (host-mapped) and `seq` published in *flag behind every output.

@@ -747,7 +747,8 @@ moe_status check_router(const char* who, const moe_router* r, int T, int E, int 
                 "%s: n_group=%d must divide E=%d and be at most 64", who, r->n_group, E);
   MOE_CHECK_ARG(r->topk_group >= 1 && r->topk_group <= r->n_group, "%s: topk_group=%d must be in [1, n_group=%d]", who,
                 r->topk_group, r->n_group);
-  const int most = std::min(r->topk_group * (E / r->n_group), kRouteMaxK);
+  static_assert(kScoredMaxK == kRouteMaxK, "ids and words of a row in LDS");
+  const int most = router_most(*r, E);
   MOE_CHECK_ARG(k >= 1 && k <= most, "%s: k=%d must be in [1, min(topk_group * E / n_group, 16)] = [1, %d]", who, k,
                 most);
   return MOE_OK;
@@ -827,7 +828,8 @@ extern "C" moe_status moe_route_scored_permute(const moe_router* r, const float*
                                                int32_t* perm, int32_t* inv, moe_stream_t stream) {
   moe_status st = check_router("moe_route_scored_permute", r, T, E, k);
   if (st != MOE_OK) return st;
-  MOE_CHECK_ARG((long long)T * k <= (1 << 17), "moe_route_scored_permute: T*k = %lld exceeds 131072", (long long)T * k);
+  MOE_CHECK_ARG((long long)T * k <= kScoredMaxRows, "moe_route_scored_permute: T*k = %lld exceeds %d", (long long)T * k,
+                kScoredMaxRows);
   MOE_CHECK_ARG(counts && offsets && (T == 0 || (logits && topk_ids && topk_w && perm && inv)),
                 "moe_route_scored_permute: null pointer");
   RouterP R = router_params(r, logits, E);

@@ -489,8 +489,11 @@ moe_status moe_cache_use_copy_engine(moe_cache* c, int on);
 
 /* Decode and prefill steps of `layer` (-1: of every layer) route by *r
  * (moe_route_scored_permute; the step's renormalize is not used) instead of
- * moe_route; r null: by moe_route again.  *r is copied; its bias has to stay
- * valid.  Takes effect with the next step. */
+ * moe_route; r null: by moe_route again.  *r is copied; its bias (num_experts
+ * values on the pool's device) has to stay valid until every step that was
+ * enqueued with it has run.  Takes effect with the next step; a step whose k
+ * the router cannot serve, or whose T*k exceeds 131072, is refused before it
+ * changes anything. */
 moe_status moe_cache_use_router(moe_cache* c, int layer, const moe_router* r);
 
 /* Hits, misses and bytes copied by cache_fill since creation or reset (host). */
