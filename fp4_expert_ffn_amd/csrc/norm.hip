@@ -53,12 +53,12 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
 // Clamps to the E4M3 range, NaN kept.
 __device__ __forceinline__ float clamp_e4m3(float v) { return v != v ? v : fminf(fmaxf(v, -448.f), 448.f); }
 
-__device__ __forceinline__ uint2 encode8(const float* v, float inv) {
+__device__ __forceinline__ uint2 encode8(const float* v) {
   uint32_t d[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    int p = __builtin_amdgcn_cvt_pk_fp8_f32(clamp_e4m3(v[4 * h] * inv), clamp_e4m3(v[4 * h + 1] * inv), 0, false);
-    p = __builtin_amdgcn_cvt_pk_fp8_f32(clamp_e4m3(v[4 * h + 2] * inv), clamp_e4m3(v[4 * h + 3] * inv), p, true);
+    int p = __builtin_amdgcn_cvt_pk_fp8_f32(clamp_e4m3(v[4 * h]), clamp_e4m3(v[4 * h + 1]), 0, false);
+    p = __builtin_amdgcn_cvt_pk_fp8_f32(clamp_e4m3(v[4 * h + 2]), clamp_e4m3(v[4 * h + 3]), p, true);
     d[h] = (uint32_t)p;
   }
   return make_uint2(d[0], d[1]);
@@ -195,10 +195,9 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm(NormParams P) {
   }
   float rstd = 1.f;
   if constexpr (NORM) rstd = 1.0f / sqrtf(ss / (float)P.H + P.eps);
-  float inv = 1.f;
+  float scale = 1.f;
   if constexpr (QM == MOE_Q_FP8) {
-    const float scale = fmaxf(am * rstd / 448.0f, 1.17549435e-38f)  /* 2^-126 */;
-    inv = 1.0f / scale;
+    scale = fmaxf(am * rstd / 448.0f, 1.17549435e-38f)  /* 2^-126 */;
     if (rt == 0) static_cast<float*>(P.qs)[row] = scale;
   }
 #pragma unroll
@@ -217,7 +216,9 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm(NormParams P) {
       for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[i][j]));
       const uint32_t code = e8m0_of(quad_max(m));
       // 2^-(code - 127) as a float: 254 - code is its biased exponent (code <= 247)
-      inv = __uint_as_float((254u - code) << 23);
+      const float inv = __uint_as_float((254u - code) << 23);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] *= inv;  // a power of two: exact
       // the four codes of a 128-column tile, from lanes 0, 4, 8, 12 of its 16
       const uint32_t up = dpp_u32<kDppRowHalfMirror>(code);  // lanes l <-> 7 - l within 8: the other block
       const uint32_t pair = (lane & 4) ? (up | (code << 8)) : (code | (up << 8));
@@ -225,8 +226,12 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm(NormParams P) {
       if (c < P.H && (lane & 15) == 0)
         static_cast<uint32_t*>(P.qs)[(int64_t)(c >> 7) * P.T + row] = pair | (far << 16);
     }
+    // divided, not multiplied by the scale's reciprocal: its rounding would move values beside a tie to the other code
+    if constexpr (QM == MOE_Q_FP8)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] /= scale;
     if constexpr (QM != MOE_Q_NONE)
-      if (c < P.H) *reinterpret_cast<uint2*>(P.q + (int64_t)row * P.ldq + c) = encode8(v[i], inv);
+      if (c < P.H) *reinterpret_cast<uint2*>(P.q + (int64_t)row * P.ldq + c) = encode8(v[i]);
   }
 }
 

@@ -314,10 +314,10 @@ moe_status moe_quantize_mxfp4(const uint16_t* x, int rows, int cols, uint8_t* q,
  *                stored K-tile-major: byte j of [cols / 128][rows][4] is the
  *                scale of columns 128 kt + 32 j .. + 31 (kt the first index),
  *                the order in which moe_linear reads them.  cols % 128 == 0.
- * A code is value / scale rounded to nearest even, saturating at +-448; a
- * NaN value stays NaN (0x7F or 0xFF) and counts for no maximum.  With an
- * infinite value the fp32 scale is infinite (that value's code NaN, the
- * others 0), the E8M0 code 247 (that value +-448). */
+ * A code is the fp32 quotient value / scale rounded to nearest even,
+ * saturating at +-448; a NaN value stays NaN (0x7F or 0xFF) and counts for no
+ * maximum.  With an infinite value the fp32 scale is infinite (that value's
+ * code NaN, the others 0), the E8M0 code 247 (that value +-448). */
 typedef enum { MOE_Q_NONE = 0, MOE_Q_FP8 = 1, MOE_Q_MXFP8 = 2 } moe_qmode;
 
 /* Arguments of moe_rmsnorm.  Row strides are in elements, at least H, a
