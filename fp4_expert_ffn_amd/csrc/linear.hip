@@ -8,6 +8,7 @@
 #include <algorithm>
 
 #include "linear.h"
+#include "linear_plan.h"
 
 namespace {
 
@@ -22,7 +23,6 @@ using namespace moe;
 // where 16 columns leave CUs idle (one token, 2048 + 2048 FP8 rows of 7168:
 // 9.1 -> 6.6 us, 4.5 TB/s; 3584 + 3584 rows fill the chip with 16 columns).
 // Bound: what a CU can load (few workgroups), else HBM.
-constexpr int kSmallMaxT = 16;  // longer batches: the tile kernel
 constexpr int kU = 4;
 
 template <int QM, bool GATED, bool EXACT, int NC, int NWV>
@@ -116,15 +116,6 @@ __global__ __launch_bounds__(64 * NWV) void k_linear_small(LinParams P, int n_ti
   put(P, to, c, e.finish(P, a, u));
 }
 
-// us of a call by what a CU loads: 2 + a workgroup's KB (weights 0.032, x
-// 0.02) for each workgroup in turn; rows: weight rows a workgroup.
-float few_cost(int T, int N, int kb, int cols, int rows) {
-  const int turns = (N + cols * 256 - 1) / (cols * 256);
-  return 2.f + (float)kb * 1e-3f * ((float)rows * 0.032f + (float)T * 0.02f) * (float)turns;
-}
-
-bool eight_columns(int T, int N, int kb) { return few_cost(T, N, kb, 8, 16) < few_cost(T, N, kb, 16, 32); }
-
 template <int QM, bool GATED, bool EXACT, int NC>
 void launch_small_waves(const LinParams& P, hipStream_t s) {
   const int nt = (P.N + NC - 1) / NC, tt = (P.T + 15) / 16;
@@ -153,22 +144,6 @@ template <int QM>
 void launch_small(const LinParams& P, hipStream_t s) {
   if (P.gated) launch_small_gate<QM, true>(P, s);
   else launch_small_gate<QM, false>(P, s);
-}
-
-// Whether k_linear_small takes the call.  It is bound by what one CU can load
-// (every workgroup reads its whole weight rows and all of x), the tile kernel
-// with its split K by launches and HBM: about 7.3 us + bytes at 8 TB/s.  Both
-// estimates are fit to 1 to 17 tokens of 256 to 7168 rows of 2 to 14 KB.  One
-// token, bf16: 4096 x 4096 8.3 against 11.8 us; 16 tokens: 7168 x 2048 10.4
-// against 10.6, 7168 x 7168 27.3 against 20.1.  Decoded E4M3 (fp32 outputs)
-// costs the tiles more: 2048 x 2048 4.0 against 12.9, 7168 x 7168 15.8 against
-// 15.7.
-bool small_wins(int T, int R, bool gated, int kb, bool exact) {
-  if (T > kSmallMaxT) return false;
-  if (exact) return true;
-  const float few = gated ? std::min(few_cost(T, R / 2, kb, 8, 16), few_cost(T, R / 2, kb, 16, 32))
-                          : few_cost(T, R, kb, 16, 16);
-  return few <= 7.3f + (float)R * (float)kb * 1.25e-7f;
 }
 
 }  // namespace

@@ -25,6 +25,7 @@
 
 #include "ffn_common.h"
 #include "linear.h"
+#include "linear_plan.h"
 
 namespace moe {
 
@@ -550,47 +551,6 @@ bool linear_tile_fits(const LinParams& P) {
 }
 
 namespace {
-
-// The tile shapes and what a call of one costs, in us: a step of a tile on a
-// CU, and the rest of a call (launch, first loads, epilogue).  Measured with
-// one or two tiles a CU over 16 to 112 steps (bf16, FP8 and MXFP8 alike: a
-// step is 128 bytes of a row in each).
-struct TileShape {
-  int bm, bn;
-  float step, rest;
-};
-constexpr TileShape kShapes[] = {{256, 256, 1.25f, 10.f}, {128, 256, 0.73f, 6.f}, {128, 128, 0.47f, 5.f},
-                                 {64, 128, 0.32f, 4.5f},  {64, 64, 0.25f, 4.f}};
-constexpr int kCus = 256;
-
-struct TilePlan {
-  int shape, splits, per;
-};
-
-// The shape and the split of K with the least estimated time: tiles in
-// rounds of one a CU; a split costs the join's launch and the sums' way
-// through memory.
-TilePlan plan_tiles(int T, int R, int kb, bool exact) {
-  const int steps = (kb + 127) / 128;
-  TilePlan best{4, 1, steps};
-  float least = 1e30f;
-  for (int i = exact ? 1 : 0; i < 5; ++i) {
-    const TileShape& h = kShapes[i];
-    const int64_t tiles = (int64_t)((T + h.bm - 1) / h.bm) * ((R + h.bn - 1) / h.bn);
-    for (int sp = 1; sp <= (i == 0 ? 1 : 16) && (sp == 1 || steps >= 4 * sp); ++sp) {
-      const int per = (steps + sp - 1) / sp;
-      if ((steps + per - 1) / per != sp) continue;  // an empty run
-      const float rounds = (float)((tiles * sp + kCus - 1) / kCus);
-      const float t = rounds * (per * h.step + (rounds > 1.f ? 0.5f * h.rest : 0.f)) + h.rest +
-                      (sp > 1 ? 3.5f + (float)sp * T * R * 8e-6f / 4.f : 0.f);
-      if (t < least) {
-        least = t;
-        best = TilePlan{i, sp, per};
-      }
-    }
-  }
-  return best;
-}
 
 template <int QM, bool GATED, bool EXACT, int WM, int WN, int TM, int TN, int S>
 void launch_one(const LinParams& P, const TilePlan& pl, float* part, hipStream_t s) {
