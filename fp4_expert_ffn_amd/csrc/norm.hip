@@ -64,6 +64,26 @@ __device__ __forceinline__ uint2 encode8(const float* v) {
   return make_uint2(d[0], d[1]);
 }
 
+// The fp32 quotient by a row's scale.  The product with the rounded reciprocal
+// alone would give values beside a tie of two codes the wrong one; with its
+// remainder, exact in an FMA, divided once more the quotient is the nearest
+// value (Markstein's division).  Both are taken times the power of two that
+// brings the scale to [1, 2), so that no remainder underflows.  16384 x 7168
+// rows alone 61 us with the product and with this, 72 with `/`.
+struct RowScale {
+  float unit, s, inv;
+  __device__ __forceinline__ void set(float scale) {  // 2^-126 .. 2^120, or infinite: finite values give 0
+    const uint32_t e = __float_as_uint(scale) >> 23;
+    unit = e == 255u ? 0.f : __uint_as_float((254u - e) << 23);
+    s = e == 255u ? 1.f : scale * unit;
+    inv = 1.0f / s;
+  }
+  __device__ __forceinline__ float divide(float v) const {
+    const float t = v * unit, q = t * inv;
+    return copysignf(fmaf(fmaf(-q, s, t), inv, q), v);  // the sign: -0
+  }
+};
+
 // The E8M0 code of a block's largest magnitude: floor(log2 amax) - 8 + 127.
 // A subnormal amax lies below 2^-126: its code would be negative, so 0.
 __device__ __forceinline__ uint32_t e8m0_of(float amax) {
@@ -195,9 +215,10 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm(NormParams P) {
   }
   float rstd = 1.f;
   if constexpr (NORM) rstd = 1.0f / sqrtf(ss / (float)P.H + P.eps);
-  float scale = 1.f;
+  RowScale rs;
   if constexpr (QM == MOE_Q_FP8) {
-    scale = fmaxf(am * rstd / 448.0f, 1.17549435e-38f)  /* 2^-126 */;
+    const float scale = fmaxf(am * rstd / 448.0f, 1.17549435e-38f)  /* 2^-126 */;
+    rs.set(scale);
     if (rt == 0) static_cast<float*>(P.qs)[row] = scale;
   }
 #pragma unroll
@@ -226,10 +247,9 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm(NormParams P) {
       if (c < P.H && (lane & 15) == 0)
         static_cast<uint32_t*>(P.qs)[(int64_t)(c >> 7) * P.T + row] = pair | (far << 16);
     }
-    // divided, not multiplied by the scale's reciprocal: its rounding would move values beside a tie to the other code
     if constexpr (QM == MOE_Q_FP8)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] /= scale;
+      for (int j = 0; j < 8; ++j) v[i][j] = rs.divide(v[i][j]);
     if constexpr (QM != MOE_Q_NONE)
       if (c < P.H) *reinterpret_cast<uint2*>(P.q + (int64_t)row * P.ldq + c) = encode8(v[i]);
   }
