@@ -343,6 +343,16 @@ _E8M0 = ("float8_e8m0fnu", "uint8")
 _F32 = ("float32",)
 
 
+_NAMES = {}  # dtype -> its name: DenseLayer.forward checks some 20 tensors a call, and making the name anew costs 0.5 us
+
+
+def _type_name(dtype) -> str:
+    n = _NAMES.get(dtype)
+    if n is None:
+        n = _NAMES[dtype] = str(dtype).replace("torch.", "")
+    return n
+
+
 def _bad(what: str):
     raise MoeError(MOE_EINVAL, what)
 
@@ -358,17 +368,17 @@ class _Taken:
         possible types and its shape; the last dimension must be dense."""
         if t is None or isinstance(t, int):
             return t
-        who = f"{self.who}: {name}"
-        if str(t.dtype).replace("torch.", "") not in dtypes:
-            _bad(f"{who} is {t.dtype}, expected {' or '.join(dtypes)}")
-        if tuple(t.shape) != tuple(shape):
-            _bad(f"{who} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if not t.is_cuda:
-            _bad(f"{who} is on {t.device}, not on a GPU")
+        if _type_name(t.dtype) not in dtypes:
+            _bad(f"{self.who}: {name} is {t.dtype}, expected {' or '.join(dtypes)}")
+        if t.shape != shape:
+            _bad(f"{self.who}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        d = t.get_device()
+        if d < 0:
+            _bad(f"{self.who}: {name} is on {t.device}, not on a GPU")
         if self.device is None:
-            self.device = t.device.index
-        elif t.device.index != self.device:
-            _bad(f"{who} is on {t.device}, other arguments on cuda:{self.device}")
+            self.device = d
+        elif d != self.device:
+            _bad(f"{self.who}: {name} is on {t.device}, other arguments on cuda:{self.device}")
         self.keep.append(t)
         return t.data_ptr()
 
@@ -382,11 +392,13 @@ class _Taken:
         p = self(name, t, dtypes, shape)
         if t is None or isinstance(t, int):
             return p, 0
-        if t.shape[1] > 1 and t.stride(1) != 1:
+        if t.is_contiguous():
+            return p, 0 if shape[0] <= 1 else shape[1]
+        if shape[1] > 1 and t.stride(1) != 1:
             _bad(f"{self.who}: the rows of {name} are not dense (strides {tuple(t.stride())})")
-        if t.shape[0] <= 1:
+        if shape[0] <= 1:
             return p, 0
-        if t.stride(0) < t.shape[1]:
+        if t.stride(0) < shape[1]:
             _bad(f"{self.who}: the rows of {name} overlap (strides {tuple(t.stride())})")
         return p, t.stride(0)
 
@@ -405,7 +417,7 @@ def _current(a, what: str):
 
 
 def _is_f32(t, flag):
-    return int(flag) if t is None or isinstance(t, int) else int(str(t.dtype) == "torch.float32")
+    return int(flag) if t is None or isinstance(t, int) else int(_type_name(t.dtype) == "float32")
 
 
 def norm_args(*, x, weight=None, eps=1e-6, residual=None, residual_out=None, out=None, q=None, q_scale=None,

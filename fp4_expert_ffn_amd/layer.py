@@ -179,6 +179,8 @@ class DenseLayer:
     def __init__(self, *, H, I, fmt, max_tokens, norm_weight, gate_up, down, gate_up_scale=None, down_scale=None,
                  eps=1e-6, device="cuda"):
         dev, T = torch.device(device), max(max_tokens, 1)
+        if fmt == "mxfp8" and (H % 128 or I % 128):
+            raise L.MoeError(L.MOE_EINVAL, f"DenseLayer: MXFP8 rows need H and I in multiples of 128 (H={H}, I={I})")
         self.H, self.I, self.fmt, self.max_tokens, self.eps = H, I, fmt, T, eps
         self.norm_weight, self.gate_up, self.down = norm_weight, gate_up, down
         self.gate_up_scale, self.down_scale = gate_up_scale, down_scale
@@ -204,14 +206,14 @@ class DenseLayer:
         return self.q[:T * n].view(T, n), s
 
     def _linear(self, residual):
-        """Arguments of the two products with the present weights, the second's sum on residual [T, H]."""
+        """Arguments of the two products with the present weights, the second's sum on residual [T, H].
+        Their x are the layer's own buffers, taken as addresses."""
         T, quant = residual.shape[0], self.fmt != "bf16"
-        nq, ns = self._rows(T, self.H) if quant else (self.n[:T], None)
-        hq, hs = self._rows(T, self.I) if quant else (self.h[:T], None)
-        up = L.linear_args(x=nq, w=self.gate_up, fmt=self.fmt, x_scale=ns, w_scale=self.gate_up_scale, act="silu",
-                           gated=True, out=self.h[:T])
-        down = L.linear_args(x=hq, w=self.down, fmt=self.fmt, x_scale=hs, w_scale=self.down_scale,
-                             residual=residual, out=self.out[:T])
+        q, s = (self.q.data_ptr(), self.q_scale.data_ptr()) if quant else (None, None)
+        up = L.linear_args(x=q or self.n.data_ptr(), T=T, K=self.H, w=self.gate_up, fmt=self.fmt, x_scale=s,
+                           w_scale=self.gate_up_scale, act="silu", gated=True, out=self.h[:T])
+        down = L.linear_args(x=q or self.h.data_ptr(), T=T, K=self.I, w=self.down, fmt=self.fmt, x_scale=s,
+                             w_scale=self.down_scale, residual=residual, out=self.out[:T])
         if self._ws is not None:
             for a in (up, down):
                 a.workspace, a.workspace_bytes = self._ws.data_ptr(), self._ws.numel()
@@ -224,6 +226,8 @@ class DenseLayer:
         assert T <= self.max_tokens
         if T == 0:
             return self.out[:0]
+        if x.get_device() != self.out.get_device():
+            raise L.MoeError(L.MOE_EINVAL, f"DenseLayer.forward: x is on {x.device}, the layer on {self.out.device}")
         kept = x if residual is None else self.residual[:T]  # the sum that goes on
         for t, buf in ((x, self.out),) if residual is None else ((x, self.residual), (residual, self.residual)):
             if _other_rows(t, buf[:T]):
@@ -231,10 +235,10 @@ class DenseLayer:
                                                "the call writes: copy it first")
         up, down = self._linear(kept)
         quant = self.fmt != "bf16"
-        nq, ns = self._rows(T, self.H) if quant else (self.n[:T], None)
+        rows = ({"q": self.q.data_ptr(), "q_scale": self.q_scale.data_ptr(), "qmode": self.fmt} if quant else
+                {"out": self.n.data_ptr()})
         norm = L.norm_args(x=x, weight=self.norm_weight, eps=self.eps, residual=residual,
-                           residual_out=None if residual is None else kept,
-                           **({"q": nq, "q_scale": ns, "qmode": self.fmt} if quant else {"out": nq}))
+                           residual_out=None if residual is None else kept, **rows)
         L.moe_rmsnorm(norm, stream)
         L.moe_linear(up, stream)
         if quant:

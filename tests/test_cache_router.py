@@ -28,6 +28,9 @@ class Bias:
     def numel(self):
         return self.n
 
+    def get_device(self):
+        return self.device.index
+
     def is_contiguous(self):
         return True
 

@@ -90,3 +90,19 @@ def test_scale_buffer_holds_the_scales_alone():
     need_gpu()
     for fmt, size in (("mxfp8", 300 * 384 // 32), ("fp8", 300 * 4)):
         assert dense(fmt)[0].q_scale.numel() == size
+
+
+def test_refusals():
+    need_gpu()
+    import fp4_expert_ffn_amd as m
+    from fp4_expert_ffn_amd.layer import DenseLayer
+    layer, _, _, _ = dense("mxfp8")
+    x = _rand(1, 5, layer.H).to(torch.bfloat16)
+    for bad, msg in ((x, "cpu"), (x.to(DEV).float(), "float32"), (x.to(DEV)[:, :128], "shape"),
+                     (x.to(DEV)[:, None], "shape")):
+        with pytest.raises(m.MoeError) as e:
+            layer.forward(bad)
+        assert e.value.status == 1 and msg in str(e.value)
+    with pytest.raises(m.MoeError) as e:
+        DenseLayer(H=256, I=200, fmt="mxfp8", max_tokens=4, norm_weight=None, gate_up=None, down=None, device=DEV)
+    assert "128" in str(e.value)
