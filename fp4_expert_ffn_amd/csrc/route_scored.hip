@@ -80,9 +80,9 @@ __device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
 __device__ __forceinline__ double sigmoid64(double l) { return l != l ? 0.0 : 1.0 / (1.0 + exp(-l)); }
 
 // exp(d) for d <= 0 within 2^-41 of it: 2^n times the Taylor sum of degree 10
-// on |r| <= ln 2 / 2 (next term 2^-42).
+// on |r| <= ln 2 / 2 (next term 2^-42).  From -746 down (-inf among it) 0.
 __device__ __forceinline__ double exp_neg64(double d) {
-  const double x = fmax(d, -745.0);
+  const double x = fmax(d, -746.0);
   const double n = rint(x * 1.4426950408889634);
   double r = fma(n, -0.6931471805599453, x);
   r = fma(n, -2.3190468138462996e-17, r);  // ln 2 = 0.6931471805599453 + 2.3190468138462996e-17

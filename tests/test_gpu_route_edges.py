@@ -1,6 +1,6 @@
 """Scored routing where its fast choice works at its limits, against the rule in
-64 bits: NaN keys at every place of a lane, and groups whose two best keys
-cancel."""
+64 bits: NaN keys at every place of a lane, groups whose two best keys cancel,
+and weights of experts at -inf beside tiny ones."""
 import itertools
 
 import numpy as np
@@ -52,3 +52,20 @@ def test_groups_whose_best_keys_cancel(m, E, G, score, big):
     bias[rng.integers(0, gs, G) + gs * np.arange(G)] = big
     check(m, logits, 2, score=score, n_group=G, topk_group=2, group_rank="top2", bias=bias)
     check(m, logits[:40], 2, score=score, n_group=G, topk_group=G - 1, group_rank="top2", bias=bias)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gap", [0.0, 300.0, 700.0])
+@pytest.mark.parametrize("E", [3, 40, 300])
+def test_infinitely_low_logits_weigh_nothing(m, E, gap):
+    """The largest logit kept out by its bias, one `gap` below it taken together with logits of -inf: their weight is
+    0, however small the sum that divides them."""
+    need_gpu()
+    logits = np.full((70, E), -np.inf, np.float32)
+    logits[:, 0] = 800.0
+    logits[:, 1] = 800.0 - gap
+    bias = np.zeros(E, np.float32)
+    bias[0] = -np.inf
+    for rows in (logits, logits[:1]):
+        check(m, rows, 2, score="softmax", bias=bias)
+        check(m, rows, 2, score="softmax", bias=bias, renormalize=False)
