@@ -11,11 +11,12 @@
 // against the time of a large library product at its 1.40 (bf16) and 3.09
 // (FP8) PFLOP/s: 2048 x 2048 bf16 36 us (24.5; the library's own product of
 // this size, without the epilogue, 34.1), 7168 x 2048 FP8 75 us (39; 62.6), 2
-// x 2048 x 7168 MXFP8 with SwiGLU 92 us (78).  Counters there: matrix cores
-// busy 0.31, 0.29 and 0.53 of the cycles, texture unit 0.33, 0.40 and 0.44,
-// LDS conflicts under 1 %, operand bytes from HBM once.  The FP8 case is 448
-// tiles on 256 CUs, a second round three quarters full; 128-row tiles round
-// better and load more bytes a product: 91 us.
+// x 2048 x 7168 MXFP8 with SwiGLU 92 us (78); cards and runs differ by 2 %,
+// bf16 by 5.  Counters there: matrix cores busy 0.31, 0.29 and 0.53 of the
+// cycles, texture unit 0.33, 0.40 and 0.44, LDS conflicts under 1 %; the L2s
+// fetch 2.4, 1.9 and 3.0 times the bytes of x, w and residual.  The FP8 case
+// is 448 tiles on 256 CUs, a second round three quarters full; 128-row tiles
+// round better and load more bytes a product: 91 us.
 //
 // EXACT (fp32 outputs of E4M3): the FP8 instructions cut small products, so
 // the codes are decoded to bf16: four matrix instructions and the decoding in
@@ -259,8 +260,8 @@ __global__ __launch_bounds__(64 * WM* WN) __attribute__((amdgpu_waves_per_eu(2, 
   // Fragment j of the weights against half h of x.  S = 2: part 1 of step s
   // is loaded beside the first half, part 2 beside the second, spread between
   // the matrix instructions: issued together they would hold back every
-  // wave's instructions behind the texture unit (76 -> 73 us, 95 -> 92 us at
-  // the FP8 and MXFP8 prefills).
+  // wave's instructions behind the texture unit (3 us less at the FP8
+  // and MXFP8 prefills above).
   auto mma_j = [&](auto jc, auto hc) __attribute__((always_inline)) {
     constexpr int j = decltype(jc)::value, h = decltype(hc)::value;
     constexpr int from = S == 2 && h == 1 ? kPart1 : 0;           // loads [from, to) beside this half

@@ -11,7 +11,7 @@
 // Bound: HBM (a few flops a byte); with few rows, one memory latency.  16384
 // x 7168, bf16 residual in and out, MXFP8 out (826 MB): 145 us, 5.7 TB/s; a
 // copy of 1 GiB reaches 5.0.  1027 x 2048, fp32 residual, FP8 and bf16 out (27
-// MB): 7.4 us.  One row of 7168: 2.4 us, one of 64 2.1.
+// MB): 7.8 us.  One row of 7168: 2.5 us, one of 64 2.1.
 #include <algorithm>
 
 #include "common.h"

@@ -20,8 +20,8 @@
 // that had it.  Bound: VALU issue and the latency of dependent cross-lane
 // steps (the logits' bytes need a tenth of the time), for few rows a chain of
 // one memory latency, the rounds and the scan.  Kernel times at 256 experts
-// in 8 groups, k = 8: one token 7.0 us; 16384 tokens 24 us for the rows, 3 + 3
-// for the permutation; 4099 tokens of 128 experts without groups 8.5 + 3 + 3.
+// in 8 groups, k = 8: one token 7.4 us; 16384 tokens 27 us for the rows, 5 + 4
+// for the permutation; 4099 tokens of 128 experts without groups 10 + 5 + 4.
 #include <algorithm>
 #include <type_traits>
 
