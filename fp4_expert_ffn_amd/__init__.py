@@ -10,6 +10,7 @@ from ._lib import (  # noqa: F401
     moe_cache_pin_resident, moe_cache_prefetch_layer, moe_cache_prefill_step, moe_cache_reset, moe_cache_resize, moe_cache_stats, moe_cache_use_copy_engine, moe_cache_use_router, moe_combine, moe_debug_fp4_codes, moe_dequant_blob, moe_expert_ffn, moe_expert_ffn_noalloc,
     moe_expert_ffn_traced, moe_expert_ffn_workspace_size, moe_last_error, moe_layer, moe_layer_traced, moe_permute, moe_prepack_expert, moe_quantize_mxfp4, moe_route,
     LinearArgs, linear_args, moe_linear, moe_linear_workspace_size,
+    GroupedArgs, LogprobArgs, grouped_args, logprob_args, moe_combine_bf16, moe_linear_grouped, moe_logprobs, moe_logprobs_workspace_size,
     NormArgs, Router, moe_route_scored, moe_route_scored_permute, router, moe_quantize_fp8, moe_rmsnorm, norm_args,
     moe_route_permute, moe_router_logits, moe_version,
 )

@@ -101,6 +101,24 @@ class LinearArgs(ctypes.Structure):
     ]
 
 
+class GroupedArgs(ctypes.Structure):
+    _fields_ = [
+        ("lin", LinearArgs), ("x_rows", ctypes.c_int), ("E", ctypes.c_int), ("offsets", ctypes.c_void_p),
+        ("rows", ctypes.c_void_p), ("rows_div", ctypes.c_int), ("slot_of_expert", ctypes.c_void_p),
+        ("w_stride", ctypes.c_int64), ("w_scale_stride", ctypes.c_int64),
+    ]
+
+
+class LogprobArgs(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int), ("V", ctypes.c_int), ("logits", ctypes.c_void_p), ("logits_f32", ctypes.c_int),
+        ("ld", ctypes.c_int64), ("scale", ctypes.c_float), ("ids", ctypes.c_void_p), ("logprob", ctypes.c_void_p),
+        ("rank", ctypes.c_void_p), ("entropy", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("k", ctypes.c_int),
+        ("top_ids", ctypes.c_void_p), ("top_logprob", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 class ExpertCanonical(ctypes.Structure):
     _fields_ = [
         ("fmt", ctypes.c_int32), ("H", ctypes.c_int32), ("I", ctypes.c_int32),
@@ -113,7 +131,7 @@ class ExpertCanonical(ctypes.Structure):
 SCORE = {"softmax": 0, "sigmoid": 1}
 GROUP_RANK = {"max": 0, "top2": 1}
 FN = {"none": 0, "silu": 1, "gelu_tanh": 2, "gelu_erf": 3, "relu": 4}
-QMODE = {"none": 0, "fp8": 1, "mxfp8": 2}
+QMODE = {"none": 0, "fp8": 1, "mxfp8": 2, "fp8_block": 3}
 
 # name -> (restype, argtypes); the exported C ABI (include/moe.h)
 _vp, _i, _sz, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
@@ -141,6 +159,10 @@ SIGNATURES = {
     "moe_quantize_fp8": (_i, [_vp, _i64, _i, _i, _i, _vp, _vp, _vp]),
     "moe_linear_workspace_size": (_sz, [ctypes.POINTER(LinearArgs)]),
     "moe_linear": (_i, [ctypes.POINTER(LinearArgs), _vp]),
+    "moe_linear_grouped": (_i, [ctypes.POINTER(GroupedArgs), _vp]),
+    "moe_combine_bf16": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp]),
+    "moe_logprobs_workspace_size": (_sz, [ctypes.POINTER(LogprobArgs)]),
+    "moe_logprobs": (_i, [ctypes.POINTER(LogprobArgs), _vp]),
     "moe_dequant_blob": (_i, [_vp, _i, _vp, _vp]),
     "moe_debug_fp4_codes": (_i, [ctypes.POINTER(FfnArgs), _i, _vp, _vp, _vp]),
     "moe_cache_create": (_vp, [_i, _sz, _vp, _i, _i]),
@@ -324,6 +346,16 @@ def moe_combine(y, inv, topk_w, y_shared, T, k, H, out, stream=None):
            "moe_combine")
 
 
+def moe_combine_bf16(y, inv, topk_w, y_shared, T, k, H, out, stream=None):
+    """moe_combine of bf16 expert outputs y [T*k,H] and y_shared [T,H] or None."""
+    t = _Taken("moe_combine_bf16")
+    yp, sp = t.dense("y", y, _BF16, (T * k, H)), t.dense("y_shared", y_shared, _BF16, (T, H))
+    ip, wp = _flat(t, "inv", inv, _I32, T * k), _flat(t, "topk_w", topk_w, _F32, T * k)
+    op = t.dense("out", out, _BF16, (T, H))
+    _current(t, "moe_combine_bf16")
+    _check(lib().moe_combine_bf16(yp, ip, wp, sp, T, k, H, op, stream_handle(stream)), "moe_combine_bf16")
+
+
 def moe_quantize_mxfp4(x, rows, cols, q, s, stream=None):
     _check(lib().moe_quantize_mxfp4(ptr(x), rows, cols, ptr(q), ptr(s), stream_handle(stream)), "moe_quantize_mxfp4")
 
@@ -341,6 +373,7 @@ _BF16 = ("bfloat16", "int16", "uint16")
 _E4M3 = ("float8_e4m3fn", "uint8")
 _E8M0 = ("float8_e8m0fnu", "uint8")
 _F32 = ("float32",)
+_I32 = ("int32",)
 
 
 _NAMES = {}  # dtype -> its name: DenseLayer.forward checks some 20 tensors a call, and making the name anew costs 0.5 us
@@ -407,6 +440,15 @@ class _Taken:
         return a
 
 
+def _flat(t, name, v, dtypes, need):
+    """Address of a dense tensor of at least `need` values, in any shape."""
+    if v is None or isinstance(v, int):
+        return v
+    if v.numel() < need:
+        _bad(f"{t.who}: {name} has {v.numel()} values, expected at least {need}")
+    return t.dense(name, v, dtypes, v.shape)
+
+
 def _current(a, what: str):
     """The call's tensors must lie on the current device (its stream runs the kernels)."""
     d = a.device if isinstance(a, _Taken) else getattr(a, "_device", None)
@@ -424,7 +466,7 @@ def norm_args(*, x, weight=None, eps=1e-6, residual=None, residual_out=None, out
               qmode="none", T=None, H=None, weight_f32=False, residual_f32=False) -> NormArgs:
     """Arguments of moe_rmsnorm: x [T,H] bf16; weight [H] and residual [T,H] bf16 or fp32 (taken from
     the tensors; the flags are for raw addresses); residual_out like residual; out [T,H] bf16; q [T,H]
-    E4M3 codes with q_scale fp32 [T] (qmode "fp8") or E8M0 [H/128, T, 4] (qmode "mxfp8")."""
+    E4M3 codes with q_scale fp32 [T] (qmode "fp8"), E8M0 [H/128, T, 4] ("mxfp8") or fp32 [H/128, T] ("fp8_block")."""
     t = _Taken("norm_args")
     if not isinstance(x, int):
         if x.dim() != 2:
@@ -445,7 +487,7 @@ def norm_args(*, x, weight=None, eps=1e-6, residual=None, residual_out=None, out
     if a.qmode == QMODE["mxfp8"]:
         a.q_scale = t.dense("q_scale", q_scale, _E8M0, (H // 128, T, 4))
     else:
-        a.q_scale = t.dense("q_scale", q_scale, _F32, (T,))
+        a.q_scale = t.dense("q_scale", q_scale, _F32, (H // 128, T) if a.qmode == QMODE["fp8_block"] else (T,))
     return t.done(a)
 
 
@@ -508,12 +550,13 @@ def moe_rmsnorm(args: NormArgs, stream=None):
 
 def moe_quantize_fp8(x, rows, cols, qmode, q, q_scale, stream=None, ldx=0):
     """8-bit rows of bf16 x [rows, cols] (tensor: its own row stride; raw address: ldx elements, 0 dense):
-    dense E4M3 codes q [rows, cols], q_scale fp32 [rows] (qmode "fp8") or E8M0 [cols/128, rows, 4] ("mxfp8")."""
+    dense E4M3 codes q [rows, cols], q_scale fp32 [rows] (qmode "fp8"), E8M0 [cols/128, rows, 4] ("mxfp8") or fp32
+    [cols/128, rows] ("fp8_block")."""
     t, qm = _Taken("moe_quantize_fp8"), QMODE.get(qmode, qmode)
     xp, ld = t.rows("x", x, _BF16, (rows, cols))
     qp = t.dense("q", q, _E4M3, (rows, cols))
     sp = (t.dense("q_scale", q_scale, _E8M0, (cols // 128, rows, 4)) if qm == QMODE["mxfp8"] else
-          t.dense("q_scale", q_scale, _F32, (rows,)))
+          t.dense("q_scale", q_scale, _F32, (cols // 128, rows) if qm == QMODE["fp8_block"] else (rows,)))
     _current(t, "moe_quantize_fp8")
     _check(lib().moe_quantize_fp8(xp, ld or ldx, rows, cols, qm, qp, sp, stream_handle(stream)), "moe_quantize_fp8")
 
@@ -521,8 +564,9 @@ def moe_quantize_fp8(x, rows, cols, qmode, q, q_scale, stream=None, ldx=0):
 def linear_args(*, x, w, out, fmt="bf16", x_scale=None, w_scale=None, bias=None, act="none", gated=False,
                 residual=None, T=None, N=None, K=None, out_f32=False) -> LinearArgs:
     """Arguments of moe_linear (workspace left empty): x [T,K] and w [R,K] bf16 (fmt "bf16") or E4M3 codes with
-    x_scale / w_scale (fmt "fp8": fp32 [T] / [R]; "mxfp8": E8M0 [K/128, T, 4] / [K/128, R, 4]); R = N, gated 2 N;
-    bias fp32 [R]; residual [T,N] bf16; out [T,N] bf16 or fp32."""
+    x_scale / w_scale (fmt "fp8": fp32 [T] / [R]; "mxfp8": E8M0 [K/128, T, 4] / [K/128, R, 4]; "fp8_block": fp32
+    [K/128, T] / [B, K/128], B = ceil(N/128), gated twice that: the gate's row blocks, then the up's); R = N, gated
+    2 N; bias fp32 [R]; residual [T,N] bf16; out [T,N] bf16 or fp32."""
     t = _Taken("linear_args")
     for name, v in (("x", x), ("w", w), ("out", out)):
         if not isinstance(v, int) and v.dim() != 2:
@@ -542,6 +586,9 @@ def linear_args(*, x, w, out, fmt="bf16", x_scale=None, w_scale=None, bias=None,
     if a.qmode == QMODE["mxfp8"]:
         a.x_scale = t.dense("x_scale", x_scale, _E8M0, (K // 128, T, 4))
         a.w_scale = t.dense("w_scale", w_scale, _E8M0, (K // 128, R, 4))
+    elif a.qmode == QMODE["fp8_block"]:
+        a.x_scale = t.dense("x_scale", x_scale, _F32, (K // 128, T))
+        a.w_scale = t.dense("w_scale", w_scale, _F32, ((2 if gated else 1) * ((N + 127) // 128), K // 128))
     else:
         a.x_scale = t.dense("x_scale", x_scale, _F32, (T,))
         a.w_scale = t.dense("w_scale", w_scale, _F32, (R,))
@@ -559,6 +606,77 @@ def moe_linear_workspace_size(args: LinearArgs) -> int:
 def moe_linear(args: LinearArgs, stream=None):
     _current(args, "moe_linear")
     _check(lib().moe_linear(ctypes.byref(args), stream_handle(stream)), "moe_linear")
+
+
+def grouped_args(*, x, x_scale, w, w_scale, offsets, out, rows=None, rows_div=1, slot_of_expert=None, bias=None,
+                 act="none", gated=False) -> GroupedArgs:
+    """Arguments of moe_linear_grouped (tensors): x [X,K] E4M3 codes with x_scale fp32 [K/128, X]; w [S,R,K] with
+    w_scale fp32 [S, B, K/128] (B as in linear_args) for S slots; offsets int32 [E+1] of the T rows of out [T,N]
+    (bf16 or fp32); rows int32 [T]: row p of the product reads row rows[p] // rows_div of x (None: row p);
+    slot_of_expert int32 [E] or None (slot e); bias fp32 [S,R]."""
+    t = _Taken("grouped_args")
+    for name, v, n in (("x", x, 2), ("w", w, 3), ("out", out, 2), ("offsets", offsets, 1)):
+        if v.dim() != n:
+            _bad(f"grouped_args: {name} has shape {tuple(v.shape)}, expected {n} dimensions")
+    (X, K), (T, N), (S, R, _), E = x.shape, out.shape, w.shape, offsets.shape[0] - 1
+    if R != (2 * N if gated else N):
+        _bad(f"grouped_args: w has {R} rows a slot, expected {2 * N if gated else N}")
+    if slot_of_expert is None and S < E:
+        _bad(f"grouped_args: {S} slots of weights for {E} experts")
+    B = (2 if gated else 1) * ((N + 127) // 128)
+    g = GroupedArgs()
+    a = g.lin
+    a.T, a.N, a.K, a.gated, a.qmode, a.fn = T, N, K, int(gated), QMODE["fp8_block"], FN.get(act, act)
+    g.x_rows, g.E, g.rows_div = X, E, int(rows_div)
+    a.x, a.ldx = t.rows("x", x, _E4M3, (X, K))
+    a.x_scale = t.dense("x_scale", x_scale, _F32, (K // 128, X))
+    a.w, a.w_scale = t.dense("w", w, _E4M3, (S, R, K)), t.dense("w_scale", w_scale, _F32, (S, B, K // 128))
+    a.bias = t.dense("bias", bias, _F32, (S, R))
+    a.out_f32 = _is_f32(out, False)
+    a.out, a.ldo = t.rows("out", out, _F32 if a.out_f32 else _BF16, (T, N))
+    g.offsets = t.dense("offsets", offsets, _I32, (E + 1,))
+    g.rows = _flat(t, "rows", rows, _I32, T)
+    g.slot_of_expert = t.dense("slot_of_expert", slot_of_expert, _I32, (E,))
+    return t.done(g)
+
+
+def moe_linear_grouped(args: GroupedArgs, stream=None):
+    _current(args, "moe_linear_grouped")
+    _check(lib().moe_linear_grouped(ctypes.byref(args), stream_handle(stream)), "moe_linear_grouped")
+
+
+def logprob_args(*, logits, ids=None, scale=1.0, logprob=None, rank=None, entropy=None, lse=None, top_ids=None,
+                 top_logprob=None, k=None, T=None, V=None, ld=0, logits_f32=False) -> LogprobArgs:
+    """Arguments of moe_logprobs (workspace left empty): logits [T,V] bf16 or fp32, ids int32 [T]; outputs logprob,
+    entropy, lse fp32 [T], rank int32 [T], top_ids int32 and top_logprob fp32 [T,k].  T, V, ld, k and logits_f32 are
+    for raw addresses."""
+    t = _Taken("logprob_args")
+    a = LogprobArgs()
+    if not isinstance(logits, int):
+        if logits.dim() != 2:
+            _bad(f"logprob_args: logits has shape {tuple(logits.shape)}, expected [T, V]")
+        T, V = logits.shape
+    for top in (top_ids, top_logprob):
+        if k is None and top is not None and not isinstance(top, int):
+            k = top.shape[-1]
+    a.T, a.V, a.k, a.scale = int(T), int(V), int(k or 0), float(scale)
+    a.logits_f32 = _is_f32(logits, logits_f32)
+    a.logits, a.ld = t.rows("logits", logits, _F32 if a.logits_f32 else _BF16, (T, V))
+    a.ld = a.ld or int(ld)
+    a.ids, a.rank = t.dense("ids", ids, _I32, (T,)), t.dense("rank", rank, _I32, (T,))
+    a.logprob, a.entropy, a.lse = (t.dense(n, v, _F32, (T,)) for n, v in (("logprob", logprob), ("entropy", entropy),
+                                                                          ("lse", lse)))
+    a.top_ids, a.top_logprob = t.dense("top_ids", top_ids, _I32, (T, k)), t.dense("top_logprob", top_logprob, _F32, (T, k))
+    return t.done(a)
+
+
+def moe_logprobs_workspace_size(args: LogprobArgs) -> int:
+    return int(lib().moe_logprobs_workspace_size(ctypes.byref(args)))
+
+
+def moe_logprobs(args: LogprobArgs, stream=None):
+    _current(args, "moe_logprobs")
+    _check(lib().moe_logprobs(ctypes.byref(args), stream_handle(stream)), "moe_logprobs")
 
 
 def moe_dequant_blob(blob, which, out, stream=None):

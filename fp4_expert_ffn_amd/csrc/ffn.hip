@@ -489,6 +489,20 @@ extern "C" moe_status moe_combine(const float* y, const int32_t* inv, const floa
   return MOE_OK;
 }
 
+extern "C" moe_status moe_combine_bf16(const uint16_t* y, const int32_t* inv, const float* topk_w,
+                                       const uint16_t* y_shared, int T, int k, int H, uint16_t* out,
+                                       moe_stream_t stream) {
+  MOE_CHECK_ARG(T >= 0 && T < 65536 && k >= 1 && k <= 16 && H > 0 && H % 8 == 0,
+                "moe_combine_bf16: bad sizes T=%d k=%d H=%d (T < 65536, k <= 16, H %% 8 == 0)", T, k, H);
+  if (T == 0) return MOE_OK;
+  MOE_CHECK_ARG(y && inv && topk_w && out, "moe_combine_bf16: null pointer");
+  MOE_CHECK_ARG((((uintptr_t)y | (uintptr_t)out | (uintptr_t)y_shared) & 15) == 0,
+                "moe_combine_bf16: y, y_shared and out must be 16-byte aligned");
+  hipError_t e = launch_combine(y, inv, topk_w, y_shared, T, k, H, out, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return set_error(MOE_EHIP, "moe_combine_bf16: launch failed: %s", hipGetErrorString(e));
+  return MOE_OK;
+}
+
 extern "C" moe_status moe_quantize_mxfp4(const uint16_t* x, int rows, int cols, uint8_t* q, uint8_t* s,
                                          moe_stream_t stream) {
   MOE_CHECK_ARG(rows >= 0 && cols > 0 && cols % 32 == 0, "moe_quantize_mxfp4: bad sizes rows=%d cols=%d", rows, cols);

@@ -8,6 +8,7 @@
 #include <algorithm>
 
 #include "linear.h"
+#include "linear_block.h"
 #include "linear_plan.h"
 
 namespace {
@@ -153,6 +154,7 @@ void launch_small(const LinParams& P, hipStream_t s) {
 extern "C" size_t moe_linear_workspace_size(const moe_linear_args* a) {
   if (!a || a->T < 1 || a->N < 1 || a->K < 1 || a->T >= (1 << 24) || a->N >= (1 << 24) || a->K >= (1 << 24))
     return 0;
+  if (a->qmode == MOE_Q_FP8_BLOCK) return linear_block_workspace(a->T, a->N, a->K, a->gated, a->out_f32);
   const int kb = a->K * (a->qmode == MOE_Q_NONE ? 2 : 1);
   const int R = a->gated ? 2 * a->N : a->N;
   const bool exact = a->qmode != MOE_Q_NONE && a->out_f32;
@@ -161,7 +163,7 @@ extern "C" size_t moe_linear_workspace_size(const moe_linear_args* a) {
 
 extern "C" moe_status moe_linear(const moe_linear_args* a, moe_stream_t stream) {
   MOE_CHECK_ARG(a, "moe_linear: null pointer");
-  MOE_CHECK_ARG(a->qmode >= MOE_Q_NONE && a->qmode <= MOE_Q_MXFP8, "moe_linear: bad qmode %d", a->qmode);
+  MOE_CHECK_ARG(a->qmode >= MOE_Q_NONE && a->qmode <= MOE_Q_FP8_BLOCK, "moe_linear: bad qmode %d", a->qmode);
   MOE_CHECK_ARG(a->fn >= MOE_FN_NONE && a->fn <= MOE_FN_RELU, "moe_linear: bad fn %d", a->fn);
   MOE_CHECK_ARG(a->T >= 0 && a->N >= 1 && a->K >= 1 && a->T < (1 << 24) && a->N < (1 << 24) && a->K < (1 << 24),
                 "moe_linear: bad sizes T=%d N=%d K=%d", a->T, a->N, a->K);
@@ -203,9 +205,10 @@ extern "C" moe_status moe_linear(const moe_linear_args* a, moe_stream_t stream) 
   P.fn = a->fn;
   P.gated = a->gated;
   P.out_f32 = a->out_f32;
+  const bool block = a->qmode == MOE_Q_FP8_BLOCK;
   const bool tile =
-      !small_wins(P.T, P.R, P.gated, P.kb, a->qmode != MOE_Q_NONE && P.out_f32) && linear_tile_fits(P);
-  const size_t need = tile ? moe_linear_workspace_size(a) : 0;
+      !block && !small_wins(P.T, P.R, P.gated, P.kb, a->qmode != MOE_Q_NONE && P.out_f32) && linear_tile_fits(P);
+  const size_t need = tile || block ? moe_linear_workspace_size(a) : 0;
   if (need > 0) {
     if (!a->workspace || a->workspace_bytes < need)
       return set_error(MOE_ENOMEM, "moe_linear: workspace %zu bytes, needs %zu", a->workspace ? a->workspace_bytes : 0,
@@ -213,7 +216,10 @@ extern "C" moe_status moe_linear(const moe_linear_args* a, moe_stream_t stream) 
     MOE_CHECK_ARG(!off(a->workspace, 16), "moe_linear: workspace must lie on a 16-byte boundary");
   }
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (tile) launch_linear_tile(P, a->qmode, a->workspace, s);
+  if (block)
+    launch_linear_block(BlockParams{P, P.T, P.K / 128, (P.N + 127) / 128, 0, 1, nullptr, nullptr, nullptr, 0, 0},
+                        a->workspace, s);
+  else if (tile) launch_linear_tile(P, a->qmode, a->workspace, s);
   else if (a->qmode == MOE_Q_NONE) launch_small<MOE_Q_NONE>(P, s);
   else if (a->qmode == MOE_Q_FP8) launch_small<MOE_Q_FP8>(P, s);
   else launch_small<MOE_Q_MXFP8>(P, s);

@@ -247,7 +247,19 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm(NormParams P) {
       if (c < P.H && (lane & 15) == 0)
         static_cast<uint32_t*>(P.qs)[(int64_t)(c >> 7) * P.T + row] = pair | (far << 16);
     }
-    if constexpr (QM == MOE_Q_FP8)
+    if constexpr (QM == MOE_Q_FP8_BLOCK) {
+      float m = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[i][j]));
+      // the 16 lanes of a block are a row of the wave
+      m = quad_max(m);
+      m = fmaxf(m, dpp_f32<kDppRowHalfMirror>(m));
+      m = fmaxf(m, dpp_f32<kDppRowMirror>(m));
+      const float scale = fmaxf(m / 448.0f, 1.17549435e-38f)  /* 2^-126 */;
+      rs.set(scale);
+      if (c < P.H && (lane & 15) == 0) static_cast<float*>(P.qs)[(int64_t)(c >> 7) * P.T + row] = scale;
+    }
+    if constexpr (QM == MOE_Q_FP8 || QM == MOE_Q_FP8_BLOCK)
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[i][j] = rs.divide(v[i][j]);
     if constexpr (QM != MOE_Q_NONE)
@@ -284,7 +296,8 @@ template <int RES>
 void launch_norm_q(const NormParams& P, int qm, hipStream_t s) {
   if (qm == MOE_Q_NONE) launch_norm<RES, MOE_Q_NONE, true>(P, s);
   else if (qm == MOE_Q_FP8) launch_norm<RES, MOE_Q_FP8, true>(P, s);
-  else launch_norm<RES, MOE_Q_MXFP8, true>(P, s);
+  else if (qm == MOE_Q_MXFP8) launch_norm<RES, MOE_Q_MXFP8, true>(P, s);
+  else launch_norm<RES, MOE_Q_FP8_BLOCK, true>(P, s);
 }
 
 constexpr int kMaxRows = 1 << 22;  // x 1024 threads: what a grid holds (below 2^32 threads)
@@ -298,8 +311,9 @@ extern "C" moe_status moe_rmsnorm(const moe_norm_args* a, moe_stream_t stream) {
   MOE_CHECK_ARG(a->T >= 0 && a->T < kMaxRows && a->H >= 8 && a->H <= 32768 && a->H % 8 == 0,
                 "moe_rmsnorm: bad sizes T=%d H=%d (T below 2^22, H a multiple of 8, at most 32768)", a->T, a->H);
   MOE_CHECK_ARG(a->eps >= 0.f, "moe_rmsnorm: eps must be >= 0");
-  MOE_CHECK_ARG(a->qmode >= MOE_Q_NONE && a->qmode <= MOE_Q_MXFP8, "moe_rmsnorm: bad qmode %d", a->qmode);
-  MOE_CHECK_ARG(a->qmode != MOE_Q_MXFP8 || a->H % 128 == 0, "moe_rmsnorm: MXFP8 rows need H %% 128 == 0, H=%d", a->H);
+  MOE_CHECK_ARG(a->qmode >= MOE_Q_NONE && a->qmode <= MOE_Q_FP8_BLOCK, "moe_rmsnorm: bad qmode %d", a->qmode);
+  MOE_CHECK_ARG((a->qmode != MOE_Q_MXFP8 && a->qmode != MOE_Q_FP8_BLOCK) || a->H % 128 == 0,
+                "moe_rmsnorm: MXFP8 and FP8_BLOCK rows need H %% 128 == 0, H=%d", a->H);
   const int64_t ld[4] = {a->ldx ? a->ldx : a->H, a->ldr ? a->ldr : a->H, a->ldo ? a->ldo : a->H,
                          a->ldq ? a->ldq : a->H};
   for (int64_t l : ld)
@@ -328,9 +342,9 @@ extern "C" moe_status moe_quantize_fp8(const uint16_t* x, int64_t ldx, int rows,
   MOE_CHECK_ARG(rows >= 0 && rows < kMaxRows && cols >= 8 && cols <= 32768 && cols % 8 == 0,
                 "moe_quantize_fp8: bad sizes rows=%d cols=%d (rows below 2^22, cols a multiple of 8, at most 32768)",
                 rows, cols);
-  MOE_CHECK_ARG(qmode == MOE_Q_FP8 || qmode == MOE_Q_MXFP8, "moe_quantize_fp8: bad qmode %d", qmode);
-  MOE_CHECK_ARG(qmode != MOE_Q_MXFP8 || cols % 128 == 0, "moe_quantize_fp8: MXFP8 rows need cols %% 128 == 0, cols=%d",
-                cols);
+  MOE_CHECK_ARG(qmode >= MOE_Q_FP8 && qmode <= MOE_Q_FP8_BLOCK, "moe_quantize_fp8: bad qmode %d", qmode);
+  MOE_CHECK_ARG(qmode == MOE_Q_FP8 || cols % 128 == 0,
+                "moe_quantize_fp8: MXFP8 and FP8_BLOCK rows need cols %% 128 == 0, cols=%d", cols);
   if (ldx == 0) ldx = cols;
   MOE_CHECK_ARG(ldx >= cols && ldx % 8 == 0, "moe_quantize_fp8: row stride %lld must be a multiple of 8, at least %d",
                 (long long)ldx, cols);
@@ -341,7 +355,8 @@ extern "C" moe_status moe_quantize_fp8(const uint16_t* x, int64_t ldx, int rows,
   const NormParams P{rows, cols, x, nullptr, nullptr, nullptr, nullptr, q, q_scale, ldx, cols, cols, cols, 0.f, 0};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (qmode == MOE_Q_FP8) launch_norm<kResNone, MOE_Q_FP8, false>(P, s);
-  else launch_norm<kResNone, MOE_Q_MXFP8, false>(P, s);
+  else if (qmode == MOE_Q_MXFP8) launch_norm<kResNone, MOE_Q_MXFP8, false>(P, s);
+  else launch_norm<kResNone, MOE_Q_FP8_BLOCK, false>(P, s);
   MOE_LAUNCHED();
   return MOE_OK;
 }

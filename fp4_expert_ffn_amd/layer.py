@@ -148,6 +148,9 @@ class MoELayer:
         raise AttributeError(name)
 
 
+_BLOCKED = ("mxfp8", "fp8_block")  # encodings with scales per block of columns: 4 bytes per 128
+
+
 def _other_rows(t, buf):
     """Whether rows t overlap the dense rows buf other than row on row, so that a kernel could write one
     before another workgroup has read it."""
@@ -165,11 +168,12 @@ class DenseLayer:
 
         r = x + residual;  out = r + W_down (silu(W_gate n) * (W_up n)),  n = norm(r)
 
-    fmt "bf16": bf16 operands; "fp8" / "mxfp8": 8-bit rows on both sides, the
-    norm writing the first product's and moe_quantize_fp8 the second's.
-    Weights: gate_up [2 I, H] (the I gate rows, then the I up rows) and down
-    [H, I], bf16 or E4M3 codes with their scales (fp32 [rows], or E8M0
-    [cols / 128, rows, 4]).  They may be replaced between calls.
+    fmt "bf16": bf16 operands; "fp8" / "mxfp8" / "fp8_block": 8-bit rows on both
+    sides, the norm writing the first product's and moe_quantize_fp8 the
+    second's.  Weights: gate_up [2 I, H] (the I gate rows, then the I up rows)
+    and down [H, I], bf16 or E4M3 codes with their scales (fp32 [rows], E8M0
+    [cols / 128, rows, 4], or fp32 [rows / 128, cols / 128]).  They may be
+    replaced between calls.
 
     Every call writes the layer's own buffers (residual, h, out, the 8-bit
     rows, the workspace): one layer serves one stream at a time, and the next
@@ -179,8 +183,8 @@ class DenseLayer:
     def __init__(self, *, H, I, fmt, max_tokens, norm_weight, gate_up, down, gate_up_scale=None, down_scale=None,
                  eps=1e-6, device="cuda"):
         dev, T = torch.device(device), max(max_tokens, 1)
-        if fmt == "mxfp8" and (H % 128 or I % 128):
-            raise L.MoeError(L.MOE_EINVAL, f"DenseLayer: MXFP8 rows need H and I in multiples of 128 (H={H}, I={I})")
+        if fmt in _BLOCKED and (H % 128 or I % 128):
+            raise L.MoeError(L.MOE_EINVAL, f"DenseLayer: {fmt} rows need H and I in multiples of 128 (H={H}, I={I})")
         self.H, self.I, self.fmt, self.max_tokens, self.eps = H, I, fmt, T, eps
         self.norm_weight, self.gate_up, self.down = norm_weight, gate_up, down
         self.gate_up_scale, self.down_scale = gate_up_scale, down_scale
@@ -190,19 +194,18 @@ class DenseLayer:
             self.n = bf16(H)
         else:
             self.q = torch.empty(T * max(H, I), dtype=torch.uint8, device=dev)
-            self.q_scale = torch.empty(T * max(H, I) // 32 if fmt == "mxfp8" else 4 * T, dtype=torch.uint8, device=dev)
-        # one workspace for every batch up to max_tokens: a captured call keeps its address
+            self.q_scale = torch.empty(T * max(H, I) // 32 if fmt in _BLOCKED else 4 * T, dtype=torch.uint8, device=dev)
         self._ws = None
-        need = 0
-        for a in self._linear(self.residual):
-            for a.T in range(1, T + 1):
-                need = max(need, L.moe_linear_workspace_size(a))
-        self._ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        self._ws = _workspace(self._linear(self.residual), T, dev)
 
     def _rows(self, T, n):
         """8-bit rows of n columns in the layer's buffers: (codes, scales)."""
-        s = (self.q_scale[:T * n // 32].view(n // 128, T, 4) if self.fmt == "mxfp8" else
-             self.q_scale[:4 * T].view(torch.float32))
+        if self.fmt == "fp8":
+            s = self.q_scale[:4 * T].view(torch.float32)
+        else:
+            s = self.q_scale[:T * n // 32].view(n // 128, T, 4)
+            if self.fmt == "fp8_block":
+                s = s.view(torch.float32)[:, :, 0]
         return self.q[:T * n].view(T, n), s
 
     def _linear(self, residual):
@@ -246,6 +249,179 @@ class DenseLayer:
             L.moe_quantize_fp8(self.h[:T], T, self.I, self.fmt, hq, hs, stream)
         L.moe_linear(down, stream)
         return self.out[:T]
+
+
+def _workspace(calls, T, dev):
+    """One workspace for the given products (LinearArgs) of every batch up to T: a captured call keeps its address."""
+    need = 0
+    for a in calls:
+        for a.T in range(1, T + 1):
+            need = max(need, L.moe_linear_workspace_size(a))
+    return torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+
+
+class BlockMoELayer:
+    """A sparse layer whose experts are E4M3 codes with one scale per 128 x 128 block: routing, then both
+    products of moe_linear_grouped on 8-bit rows, and the weighted combine.
+
+        out_t = sum_j w_tj W_down (silu(W_gate x_t) * (W_up x_t)) [+ the shared expert's]
+
+    Weights: gate_up [S, 2 I, H] (the I gate rows, then the I up rows) with fp32 scales [S, 2 ceil(I / 128),
+    H / 128], down [S, H, I] with [S, ceil(H / 128), I / 128], in S slots; slot_of_expert int32 [E] maps expert
+    to slot (None: slot e).  shared: None, or (gate_up, gate_up_scale, down, down_scale) of the always-on expert,
+    without the slots' dimension.  router as in MoELayer.
+
+    Every call writes the layer's own buffers: one layer serves one stream at a time, and the next call replaces
+    what the last returned."""
+
+    def __init__(self, *, E, k, H, I, max_tokens, gate_up, gate_up_scale, down, down_scale, slot_of_expert=None,
+                 shared=None, router=None, renormalize=True, device="cuda"):
+        if H % 128 or I % 128:
+            raise L.MoeError(L.MOE_EINVAL, f"BlockMoELayer: H and I in multiples of 128 (H={H}, I={I})")
+        dev, T = torch.device(device), max(max_tokens, 1)
+        self.E, self.k, self.H, self.I, self.max_tokens = E, k, H, I, T
+        self.gate_up, self.gate_up_scale, self.down, self.down_scale = gate_up, gate_up_scale, down, down_scale
+        self.slot_of_expert, self.shared, self.router, self.renormalize = slot_of_expert, shared, router, renormalize
+        new = lambda *n, t: torch.empty(n, dtype=t, device=dev)  # noqa: E731
+        self.logits, self.w = new(T, E, t=torch.float32), new(T, k, t=torch.float32)
+        self.ids, self.counts, self.offsets = (new(*n, t=torch.int32) for n in ((T, k), (E,), (E + 1,)))
+        self.perm, self.inv = new(T * k, t=torch.int32), new(T * k, t=torch.int32)
+        self.xq, self.xs = new(T * H, t=torch.uint8), new(T * H // 128, t=torch.float32)
+        self.h, self.y, self.out = (new(*n, t=torch.bfloat16) for n in ((T * k, I), (T * k, H), (T, H)))
+        self.hq, self.hs = new(T * k * I, t=torch.uint8), new(T * k * I // 128, t=torch.float32)
+        self._ws = None
+        if shared is not None:
+            self.shared_h, self.shared_y = new(T, I, t=torch.bfloat16), new(T, H, t=torch.bfloat16)
+            self.sq, self.ss = new(T * I, t=torch.uint8), new(T * I // 128, t=torch.float32)
+            self._ws = _workspace(self._shared(T, *self._rows(self.xq, self.xs, T, H)), T, dev)
+
+    @staticmethod
+    def _rows(q, s, T, n):
+        return q[:T * n].view(T, n), s[:T * n // 128].view(n // 128, T)
+
+    def _shared(self, T, xq, xs):
+        gu, gs, dw, ds = self.shared
+        hq, hs = self._rows(self.sq, self.ss, T, self.I)
+        a = (L.linear_args(x=xq, x_scale=xs, w=gu, w_scale=gs, fmt="fp8_block", act="silu", gated=True,
+                           out=self.shared_h[:T]),
+             L.linear_args(x=hq, x_scale=hs, w=dw, w_scale=ds, fmt="fp8_block", out=self.shared_y[:T]))
+        if self._ws is not None:
+            for p in a:
+                p.workspace, p.workspace_bytes = self._ws.data_ptr(), self._ws.numel()
+        return a
+
+    def forward(self, x, *, logits=None, w_router=None, rows=None, stream=None):
+        """x [T,H] bf16, logits fp32 [T,E] or w_router fp32 [E,H]; rows: None, or x's encoding (q, q_scale) as
+        moe_rmsnorm writes it ("fp8_block").  Returns out [T,H] (the layer's buffer)."""
+        T, k, H, I = x.shape[0], self.k, self.H, self.I
+        assert T <= self.max_tokens
+        if T == 0:
+            return self.out[:0]
+        if x.get_device() != self.out.get_device():
+            raise L.MoeError(L.MOE_EINVAL, f"BlockMoELayer.forward: x is on {x.device}, the layer on {self.out.device}")
+        if x.shape[1] != H or x.stride(1) != 1:
+            raise L.MoeError(L.MOE_EINVAL, f"BlockMoELayer.forward: x has shape {tuple(x.shape)}, expected dense rows of {H}")
+        if logits is None:
+            if not x.is_contiguous():
+                raise L.MoeError(L.MOE_EINVAL, "BlockMoELayer.forward: the router's product needs a contiguous x")
+            L.moe_router_logits(x, w_router, T, H, self.E, self.logits, stream)
+            logits = self.logits[:T]
+        r = (self.ids, self.w, self.counts, self.offsets, self.perm, self.inv)
+        if self.router is not None:
+            L.moe_route_scored_permute(self.router, logits, T, self.E, k, *r, stream)
+        else:
+            L.moe_route_permute(logits, T, self.E, k, self.renormalize, *r, stream)
+        if rows is None:
+            rows = self._rows(self.xq, self.xs, T, H)
+            L.moe_quantize_fp8(x, T, H, "fp8_block", *rows, stream)
+        xq, xs = rows
+        L.moe_linear_grouped(L.grouped_args(x=xq, x_scale=xs, w=self.gate_up, w_scale=self.gate_up_scale,
+                                            offsets=self.offsets, rows=self.perm, rows_div=k,
+                                            slot_of_expert=self.slot_of_expert, act="silu", gated=True,
+                                            out=self.h[:T * k]), stream)
+        hq, hs = self._rows(self.hq, self.hs, T * k, I)
+        L.moe_quantize_fp8(self.h[:T * k], T * k, I, "fp8_block", hq, hs, stream)
+        L.moe_linear_grouped(L.grouped_args(x=hq, x_scale=hs, w=self.down, w_scale=self.down_scale,
+                                            offsets=self.offsets, slot_of_expert=self.slot_of_expert,
+                                            out=self.y[:T * k]), stream)
+        ysh = None
+        if self.shared is not None:
+            up, down = self._shared(T, xq, xs)
+            L.moe_linear(up, stream)
+            L.moe_quantize_fp8(self.shared_h[:T], T, I, "fp8_block", *self._rows(self.sq, self.ss, T, I), stream)
+            L.moe_linear(down, stream)
+            ysh = self.shared_y[:T]
+        L.moe_combine_bf16(self.y[:T * k], self.inv, self.w, ysh, T, k, H, self.out[:T], stream)
+        return self.out[:T]
+
+
+class TokenHead:
+    """What answers with tokens behind the last layer: residual addition and RMS norm, the product with the
+    vocabulary's rows, and the log probabilities of the answer.
+
+        logits = norm(x + residual) W^T;  then moe_logprobs of scale * logits
+
+    fmt and w [V,H], w_scale as DenseLayer's weights ("bf16", "fp8", "mxfp8", "fp8_block"); logits fp32
+    (logits_f32) or bf16; k alternatives a row.  Every call writes the head's own buffers: one head serves one
+    stream at a time, and the next call replaces what the last returned."""
+
+    def __init__(self, *, H, V, fmt, max_tokens, norm_weight, w, w_scale=None, k=0, eps=1e-6, logits_f32=False,
+                 device="cuda"):
+        dev, T = torch.device(device), max(max_tokens, 1)
+        if fmt in _BLOCKED and H % 128:
+            raise L.MoeError(L.MOE_EINVAL, f"TokenHead: {fmt} rows need H in multiples of 128 (H={H})")
+        self.H, self.V, self.fmt, self.k, self.eps, self.max_tokens = H, V, fmt, k, eps, T
+        self.norm_weight, self.w, self.w_scale = norm_weight, w, w_scale
+        new = lambda *n, t=torch.float32: torch.empty(n, dtype=t, device=dev)  # noqa: E731
+        self.logits = new(T, V, t=torch.float32 if logits_f32 else torch.bfloat16)
+        self.logprob, self.entropy, self.lse, self.rank = new(T), new(T), new(T), new(T, t=torch.int32)
+        self.top_ids, self.top_logprob = (new(T, k, t=torch.int32), new(T, k)) if k else (None, None)
+        if fmt == "bf16":
+            self.n = new(T, H, t=torch.bfloat16)
+        else:
+            self.q = new(T * H, t=torch.uint8)
+            self.q_scale = new(T * H // 32 if fmt in _BLOCKED else 4 * T, t=torch.uint8)
+        self._ws = _workspace([self._linear(T)], T, dev)
+        a = self._logprobs(T, None, 1.0)
+        need = 0
+        for a.T in range(1, T + 1):
+            need = max(need, L.moe_logprobs_workspace_size(a))
+        self._lws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+
+    def _linear(self, T):
+        quant = self.fmt != "bf16"
+        q, s = (self.q.data_ptr(), self.q_scale.data_ptr()) if quant else (self.n.data_ptr(), None)
+        a = L.linear_args(x=q, T=T, K=self.H, w=self.w, fmt=self.fmt, x_scale=s, w_scale=self.w_scale,
+                          out=self.logits[:T])
+        if getattr(self, "_ws", None) is not None:
+            a.workspace, a.workspace_bytes = self._ws.data_ptr(), self._ws.numel()
+        return a
+
+    def _logprobs(self, T, ids, scale):
+        cut = lambda t: None if t is None else t[:T]  # noqa: E731
+        given = dict(ids=ids, logprob=self.logprob[:T], rank=self.rank[:T]) if ids is not None else {}
+        a = L.logprob_args(logits=self.logits[:T], scale=scale, entropy=self.entropy[:T], lse=self.lse[:T],
+                           top_ids=cut(self.top_ids), top_logprob=cut(self.top_logprob), **given)
+        if getattr(self, "_lws", None) is not None:
+            a.workspace, a.workspace_bytes = self._lws.data_ptr(), self._lws.numel()
+        return a
+
+    def forward(self, x, residual=None, ids=None, scale=1.0, stream=None):
+        """x [T,H] and residual [T,H] or None, bf16; ids int32 [T] or None; scale: 1 / temperature.  Returns the
+        outputs by name: logits, lse, entropy, with ids logprob and rank, with k top_ids and top_logprob."""
+        T = x.shape[0]
+        assert T <= self.max_tokens
+        names = ["logits", "lse", "entropy"] + (["logprob", "rank"] if ids is not None else [])
+        names += ["top_ids", "top_logprob"] if self.k else []
+        if T > 0:
+            if x.get_device() != self.logits.get_device():
+                raise L.MoeError(L.MOE_EINVAL, f"TokenHead.forward: x is on {x.device}, the head on {self.logits.device}")
+            rows = ({"q": self.q.data_ptr(), "q_scale": self.q_scale.data_ptr(), "qmode": self.fmt}
+                    if self.fmt != "bf16" else {"out": self.n.data_ptr()})
+            L.moe_rmsnorm(L.norm_args(x=x, weight=self.norm_weight, eps=self.eps, residual=residual, **rows), stream)
+            L.moe_linear(self._linear(T), stream)
+            L.moe_logprobs(self._logprobs(T, ids, scale), stream)
+        return {n: getattr(self, n)[:T] for n in names}
 
 
 def _use_routers(cache, router):

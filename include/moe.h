@@ -293,6 +293,12 @@ moe_status moe_expert_ffn_traced(const moe_ffn_args* a, moe_stream_t stream, voi
 moe_status moe_combine(const float* y, const int32_t* inv, const float* topk_w, const float* y_shared,
                        int T, int k, int H, uint16_t* out, moe_stream_t stream);
 
+/* moe_combine of bf16 expert outputs (y and y_shared bf16, as
+ * moe_linear_grouped writes them); sums in fp32.  Requires 1 <= k <= 16,
+ * T < 65536, H % 8 == 0, every row on a 16-byte boundary. */
+moe_status moe_combine_bf16(const uint16_t* y, const int32_t* inv, const float* topk_w, const uint16_t* y_shared,
+                            int T, int k, int H, uint16_t* out, moe_stream_t stream);
+
 /* MXFP4 encoding of bf16 activations, per row per 32 values (the activation
  * quantiser of the FP4 matrix-core path): shared exponent floor(log2 amax)-2
  * (E8M0, 127 for an all-zero block), elements round-to-nearest-even on the
@@ -314,11 +320,15 @@ moe_status moe_quantize_mxfp4(const uint16_t* x, int rows, int cols, uint8_t* q,
  *                stored K-tile-major: byte j of [cols / 128][rows][4] is the
  *                scale of columns 128 kt + 32 j .. + 31 (kt the first index),
  *                the order in which moe_linear reads them.  cols % 128 == 0.
+ *   MOE_Q_FP8_BLOCK: one fp32 scale per 128 columns, s = max(amax / 448,
+ *                2^-126), stored column block by column block: [cols / 128][rows].
+ *                cols % 128 == 0.  Weights in this encoding have one scale per
+ *                128 rows x 128 columns instead, see moe_linear_args.
  * A code is the fp32 quotient value / scale rounded to nearest even,
  * saturating at +-448; a NaN value stays NaN (0x7F or 0xFF) and counts for no
  * maximum.  With an infinite value the fp32 scale is infinite (that value's
  * code NaN, the others 0), the E8M0 code 247 (that value +-448). */
-typedef enum { MOE_Q_NONE = 0, MOE_Q_FP8 = 1, MOE_Q_MXFP8 = 2 } moe_qmode;
+typedef enum { MOE_Q_NONE = 0, MOE_Q_FP8 = 1, MOE_Q_MXFP8 = 2, MOE_Q_FP8_BLOCK = 3 } moe_qmode;
 
 /* Arguments of moe_rmsnorm.  Row strides are in elements, at least H, a
  * multiple of 8, and 0 means H; every pointer 16-byte aligned (q and scales:
@@ -341,7 +351,7 @@ typedef struct {
   int qmode;                /* moe_qmode: the 8-bit output                           */
   uint8_t* q;               /* [T,H] codes (required unless MOE_Q_NONE)              */
   int64_t ldq;
-  void* q_scale;            /* fp32 [T], or E8M0 [H/128][T][4]                       */
+  void* q_scale;            /* fp32 [T], E8M0 [H/128][T][4], or fp32 [H/128][T]      */
 } moe_norm_args;
 
 /* RMS norm of x + residual over each row, in one pass over the data:
@@ -376,7 +386,10 @@ typedef enum {
 /* Arguments of moe_linear.  Row strides are in elements, 0 means dense.
  * x and w rows: K bf16 values (qmode MOE_Q_NONE) or E4M3 codes with the
  * scales of their encoding (MOE_Q_FP8: fp32 [T] and [R]; MOE_Q_MXFP8: E8M0
- * [K/128][T][4] and [K/128][R][4]), R = N, or 2 N with gated. */
+ * [K/128][T][4] and [K/128][R][4]; MOE_Q_FP8_BLOCK: fp32 [K/128][T] and
+ * [B][K/128]), R = N, or 2 N with gated.  B row blocks of the weights:
+ * ceil(N / 128), where row n lies in block n / 128; gated the gate's
+ * ceil(N / 128) and then the up's, each counted from its own first row. */
 typedef struct {
   int T, N, K;              /* rows of x, columns of out, contraction                  */
   int qmode;                /* moe_qmode of x and w                                    */
@@ -412,15 +425,90 @@ size_t moe_linear_workspace_size(const moe_linear_args* a);
  * they are decoded to bf16 instead: every product exact, all sums in fp32 (and
  * block scales outside 2^-117 .. 2^119 leave the range of the decoded values).
  * A block scale of code 255 (NaN), which no encoder here writes, gives no
- * defined sums.
+ * defined sums.  MOE_Q_FP8_BLOCK: the sum over each 128 columns so, times
+ * the product of its two scales, added up in fp32.
  * [page "FreeToken qwen：...", 3rd paragraph: the layer's products; the dense
  *  product beside the experts and its epilogue are this library's reading.]
  * Requires T >= 0, N >= 1, K >= 1, rows of whole 16-byte pieces (K % 8 == 0
- * for bf16, K % 16 == 0 for FP8, K % 128 == 0 for MXFP8; strides alike, at
- * least the row), x and w on 16-byte boundaries, N and T below 2^24.
+ * for bf16, K % 16 == 0 for FP8, K % 128 == 0 for MXFP8 and FP8_BLOCK; strides
+ * in whole 16-byte pieces, at least the row), x and w on 16-byte boundaries, N and T below 2^24.
  * Errors: MOE_EINVAL, MOE_ENOMEM (workspace too small); nothing is enqueued
  * on an error. */
 moe_status moe_linear(const moe_linear_args* a, moe_stream_t stream);
+
+/* The product over the rows of routed experts, each expert's rows by its own
+ * weights: expert e's rows are offsets[e] .. offsets[e + 1] - 1 of out, its
+ * weights those of slot slot_of_expert[e]. */
+typedef struct {
+  moe_linear_args lin;          /* T rows of out; x, w, bias and scales as there (qmode
+                                   MOE_Q_FP8_BLOCK), w, w_scale and bias those of slot 0;
+                                   residual null; no workspace is read               */
+  int x_rows;                   /* rows of x (its scales: [K/128][x_rows]); without
+                                   rows at least T                                    */
+  int E;                        /* experts, 1 <= E <= 1024                            */
+  const int32_t* offsets;       /* [E+1] ascending, from moe_permute                  */
+  const int32_t* rows;          /* nullable [T]: row p of the product is row
+                                   rows[p] / rows_div of x (perm of moe_permute with
+                                   rows_div = k: the token's row); null: row p        */
+  int rows_div;                 /* >= 1 with rows                                     */
+  const int32_t* slot_of_expert;/* nullable [E]: null means slot e                    */
+  int64_t w_stride;             /* bytes from a slot's weights to the next's, a
+                                   multiple of 16; 0: dense (R * ldw)                 */
+  int64_t w_scale_stride;       /* bytes between slots' scales, a multiple of 4; 0:
+                                   dense; bias: R values a slot                       */
+} moe_grouped_args;
+
+/* moe_linear of every expert's rows in one launch.  Rows at or past
+ * offsets[E] are left as they were; an x row past x_rows is taken as the last.
+ * [page "FreeToken量子化：MoE推論のセットアップガイド", 2nd paragraph: each
+ *  token passes through only a few of the experts; block-scaled FP8 rows are
+ *  this library's reading.]
+ * Requires what moe_linear does, and x_rows * ldx below 2^32 bytes. */
+moe_status moe_linear_grouped(const moe_grouped_args* a, moe_stream_t stream);
+
+/* ------------------------------------------------------ log probabilities */
+
+/* Arguments of moe_logprobs.  z = scale * logits; every output may be null,
+ * one at least is not. */
+typedef struct {
+  int T, V;                 /* rows, tokens of the vocabulary; V < 2^30               */
+  const void* logits;       /* [T,V] bf16, or fp32 with logits_f32                    */
+  int logits_f32;
+  int64_t ld;               /* row stride in elements, at least V; 0: V               */
+  float scale;              /* > 0 and finite: 1 / temperature                        */
+  const int32_t* ids;       /* nullable [T]: the given tokens (logprob, rank)          */
+  float* logprob;           /* nullable [T]: z[id] - lse                              */
+  int32_t* rank;            /* nullable [T]: tokens in front of the given one         */
+  float* entropy;           /* nullable [T]: - sum p log p                            */
+  float* lse;               /* nullable [T]: log sum exp(z)                           */
+  int k;                    /* alternatives, 0 <= k <= min(64, V)                     */
+  int32_t* top_ids;         /* nullable [T,k]: the k largest logits, in order         */
+  float* top_logprob;       /* nullable [T,k]                                         */
+  void* workspace;          /* device scratch, >= moe_logprobs_workspace_size, 16-byte
+                               aligned; no contents carry over between calls.  Calls
+                               that share a workspace must not overlap.               */
+  size_t workspace_bytes;
+} moe_logprob_args;
+
+/* Bytes of device workspace a call with these sizes needs (0: none; the
+ * pointers need not be set). */
+size_t moe_logprobs_workspace_size(const moe_logprob_args* a);
+
+/* Log probabilities of the given tokens, their ranks, the rows' entropies and
+ * the k most likely tokens, in one read of the logits.
+ * [page "FreeToken の概要": a server of tokens; the operator is this library's
+ *  reading.]
+ * The order is that of moe_route: larger logits first, equal ones by the lower
+ * id, NaN below -inf.  exp(z - max) is taken as 1 where the logit equals the
+ * row's largest, so that a row of equal logits is uniform, a row of nothing but
+ * -inf too, and tokens at +inf share the row; other tokens then have -inf.  A
+ * row with a NaN logit gives NaN for every log probability, entropy and lse
+ * (its order stays defined).  A negative id is no token: log probability 0,
+ * rank -1; an id from V on: NaN, -1; a given NaN logit: NaN, -1.
+ * Sums are held in fp32 per thread and joined in 64 bits.
+ * Errors: MOE_EINVAL, MOE_ENOMEM (workspace too small); nothing is enqueued on
+ * an error. */
+moe_status moe_logprobs(const moe_logprob_args* a, moe_stream_t stream);
 
 /* Debug: the MXFP4 encodings an FP4 matrix-core call (amode MXFP4) left in
  * its workspace, copied to canonical layout, for the bit-exact tests of the
