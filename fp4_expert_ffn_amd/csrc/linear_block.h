@@ -63,6 +63,14 @@ __device__ __forceinline__ RowBlock find_row_block(const BlockParams& B, int b) 
   return r;
 }
 
+// Row blocks of BM rows of all experts.
+template <int BM>
+__device__ __forceinline__ int count_row_blocks(const BlockParams& B) {
+  int n = 0;
+  for (int e = threadIdx.x & 63; e < B.E; e += 64) n += (max(B.offsets[e + 1] - B.offsets[e], 0) + BM - 1) / BM;
+  return __builtin_amdgcn_readlane(wave_scan(n), 63);
+}
+
 // Row of x that row p of the product reads.
 __device__ __forceinline__ int x_row(const BlockParams& B, int p) {
   const uint32_t r = B.rows ? (uint32_t)B.rows[p] / (uint32_t)B.div : (uint32_t)p;
@@ -70,11 +78,11 @@ __device__ __forceinline__ int x_row(const BlockParams& B, int p) {
 }
 
 // The expert's weights, scales and bias in place of slot 0's.
-__device__ __forceinline__ void to_slot(BlockParams& B, int e) {
+__device__ __forceinline__ void to_slot(const BlockParams& B, int e, LinParams& P) {
   const int64_t s = B.slot ? B.slot[e] : e;
-  B.L.w += s * B.w_stride;
-  B.L.ws = static_cast<const float*>(B.L.ws) + s * B.ws_stride;
-  if (B.L.bias) B.L.bias += s * B.L.R;
+  P.w += s * B.w_stride;
+  P.ws = static_cast<const float*>(P.ws) + s * B.ws_stride;
+  if (P.bias) P.bias += s * P.R;
 }
 
 // Most row blocks of BM rows that T rows of E experts can make.
@@ -82,6 +90,11 @@ inline long long most_row_blocks(int T, int E, int bm) {
   const long long used = T < E ? T : E;
   return used + (T - used) / bm;
 }
+
+struct TilePlan;
+// The tile kernel (linear_block_tile.hip).  False: the call's strides do not fit it.
+bool block_tile_fits(const BlockParams& B);
+void launch_block_tile(const BlockParams& B, const TilePlan& pl, void* workspace, hipStream_t s);
 
 size_t linear_block_workspace(int T, int N, int K, bool gated, bool out_f32);
 void launch_linear_block(const BlockParams& B, void* workspace, hipStream_t s);

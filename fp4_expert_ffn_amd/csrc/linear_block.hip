@@ -9,6 +9,7 @@
 #include <algorithm>
 
 #include "linear_block.h"
+#include "linear_block_plan.h"
 
 namespace {
 
@@ -27,16 +28,16 @@ __global__ __launch_bounds__(64 * NWV) void k_block_small(BlockParams B, int n_t
   __shared__ float part[NWV][NB][256];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n0 = (int)(blockIdx.x % n_tiles) * NC;
-  int t0 = (int)(blockIdx.x / n_tiles) * 16, end = B.L.T;
+  LinParams P = B.L;
+  int t0 = (int)(blockIdx.x / n_tiles) * 16, end = P.T;
   if constexpr (GROUPED) {
     const RowBlock rb = find_row_block<16>(B, (int)(blockIdx.x / n_tiles));
     if (rb.e < 0) return;  // whole workgroups leave
     t0 = rb.t0;
     end = rb.end;
     if (t0 >= end) return;
-    to_slot(B, rb.e);
+    to_slot(B, rb.e, P);
   }
-  const LinParams& P = B.L;
   const int r = lane & 15, g = lane >> 4;
   // rows past the end re-read the last one
   int t = min(t0 + r, end - 1);
@@ -134,11 +135,23 @@ void launch_small(const BlockParams& B, hipStream_t s) {
 
 namespace moe {
 
-size_t linear_block_workspace(int T, int N, int K, bool gated, bool out_f32) { return 0; }
+size_t linear_block_workspace(int T, int N, int K, bool gated, bool out_f32) {
+  const int R = gated ? 2 * N : N;
+  if (block_small_wins(T, R, gated, K, out_f32)) return 0;
+  const TilePlan pl = plan_block_tiles(T, R, K, out_f32);
+  return pl.splits > 1 ? (size_t)pl.splits * T * R * sizeof(float) : 0;
+}
 
 void launch_linear_block(const BlockParams& B, void* workspace, hipStream_t s) {
-  if (B.offsets) launch_small<true>(B, s);
-  else launch_small<false>(B, s);
+  const LinParams& P = B.L;
+  const bool fits = block_tile_fits(B);
+  if (B.offsets) {
+    if (!fits || grouped_small_wins(P.T, B.E)) launch_small<true>(B, s);
+    else launch_block_tile(B, plan_grouped_tiles(P.T, B.E, P.K, P.out_f32), nullptr, s);
+  } else {
+    if (!fits || block_small_wins(P.T, P.R, P.gated, P.K, P.out_f32)) launch_small<false>(B, s);
+    else launch_block_tile(B, plan_block_tiles(P.T, P.R, P.K, P.out_f32), workspace, s);
+  }
 }
 
 }  // namespace moe
