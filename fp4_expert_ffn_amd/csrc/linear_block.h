@@ -95,6 +95,8 @@ struct TilePlan;
 // The tile kernel (linear_block_tile.hip).  False: the call's strides do not fit it.
 bool block_tile_fits(const BlockParams& B);
 void launch_block_tile(const BlockParams& B, const TilePlan& pl, void* workspace, hipStream_t s);
+// Tiles of 256 x 256 (linear_block_big.hip): bf16 outputs, K not split.
+void launch_block_big(const BlockParams& B, hipStream_t s);
 
 size_t linear_block_workspace(int T, int N, int K, bool gated, bool out_f32);
 void launch_linear_block(const BlockParams& B, void* workspace, hipStream_t s);

@@ -40,9 +40,6 @@ void launch_one(const BlockParams& B, const TilePlan& pl, float* part, hipStream
 
 template <bool GATED, bool EXACT, bool GROUPED>
 void launch_shape(const BlockParams& B, const TilePlan& pl, float* part, hipStream_t s) {
-  if constexpr (!EXACT) {
-    if (pl.shape == 0) return launch_one<GATED, EXACT, GROUPED, 2, 4, 8, 4, 2>(B, pl, part, s);
-  }
   if (pl.shape == 1) launch_one<GATED, EXACT, GROUPED, 2, 4, 4, 4, 3>(B, pl, part, s);
   else if (pl.shape == 2) launch_one<GATED, EXACT, GROUPED, 2, 2, 4, 4, 2>(B, pl, part, s);
   else if (pl.shape == 3) launch_one<GATED, EXACT, GROUPED, 2, 2, 2, 4, 3>(B, pl, part, s);
@@ -59,6 +56,7 @@ void launch_out(const BlockParams& B, const TilePlan& pl, float* part, hipStream
 
 void launch_block_tile(const BlockParams& B, const TilePlan& pl, void* workspace, hipStream_t s) {
   float* part = static_cast<float*>(workspace);
+  if (pl.shape == 0) return launch_block_big(B, s);
   if (B.offsets) B.L.gated ? launch_out<true, true>(B, pl, part, s) : launch_out<false, true>(B, pl, part, s);
   else B.L.gated ? launch_out<true, false>(B, pl, part, s) : launch_out<false, false>(B, pl, part, s);
 }

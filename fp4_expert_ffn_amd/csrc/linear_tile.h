@@ -41,6 +41,126 @@ struct LinTiles {
   float* part;           // splits > 1: the sums [splits][T][R]
 };
 
+// The epilogue of a tile from its sums: rows t0 .. t_end - 1 at most, output
+// columns from n0 on; bias and, MOE_Q_FP8, row scales in LDS; ring: LDS that
+// nothing reads or fills any more, 16 rows of SR floats a wave.
+template <int QM, bool GATED, int WM, int WN, int TM, int TN>
+__device__ __forceinline__ void tile_epilogue(const LinParams& P, const LinTiles& G, lf32x4_t (&acc)[TM][TN], uint8_t* ring,
+                                              const float* s_bias, const float* s_ws, const float* s_xs, int t0, int t_end,
+                                              int n0) {
+  constexpr int OC = GATED ? TN / 2 : TN;            // 16-column groups of output a wave
+  constexpr int SR = OC * 16 + 4;                    // staging row, floats
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int r16 = lane & 15, g = lane >> 4;
+  // ---- epilogue.  Lane: token r16 of a 16-token group, weight rows 4 g + v
+  // of a group: scales, bias, activation and gate in place; then, through LDS
+  // in fp32, rows of 8 columns a lane: the residual and whole 16-byte stores.
+  constexpr int LPR = OC * 2, RP = 64 / LPR, PS = 16 / RP;  // lanes a row, rows a pass, passes
+  const int er = lane / LPR, ec = n0 + wn * OC * 16 + (lane % LPR) * 8;
+  const int tw = t0 + wm * TM * 16;  // the wave's first token
+  // residual rows, four groups ahead of their stores (out may be the
+  // residual: a lane reads and writes the same places)
+  constexpr int RD = TM < 4 ? TM : 4;
+  uint4 rr[RD][PS];
+  const bool whole = ec + 8 <= P.N && G.vec_out && (G.vec_res || !P.res);
+  auto load_res = [&](int i) __attribute__((always_inline)) {
+    if (P.res && whole) {
+#pragma unroll
+      for (int p = 0; p < PS; ++p) {
+        const int t = tw + i * 16 + p * RP, rows = t_end - t;  // uniform
+        if (rows > 0)
+          rr[i % RD][p] = *reinterpret_cast<const uint4*>(P.res + (int64_t)t * P.ldr +
+                                                          (uint32_t)(min(er, rows - 1) * (int)P.ldr + ec));
+      }
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < RD; ++i) load_res(i);
+  wait_loads<0>();
+  lds_sync();  // nothing reads or fills the ring any more: its memory takes the staging rows
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+    const float4 b4 = *reinterpret_cast<const float4*>(s_bias + (wn * TN + j) * 16 + 4 * g);
+    const float bj[4] = {b4.x, b4.y, b4.z, b4.w};
+    float wj[4] = {1.f, 1.f, 1.f, 1.f};
+    if constexpr (QM == MOE_Q_FP8) {
+      const float4 w4 = *reinterpret_cast<const float4*>(s_ws + (wn * TN + j) * 16 + 4 * g);
+      wj[0] = w4.x, wj[1] = w4.y, wj[2] = w4.z, wj[3] = w4.w;
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      float xs = 1.f;
+      if constexpr (QM == MOE_Q_FP8) xs = s_xs[(wm * TM + i) * 16 + r16];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        if constexpr (QM == MOE_Q_FP8) acc[i][j][v] = fmaf(acc[i][j][v], xs * wj[v], bj[v]);
+        else acc[i][j][v] += bj[v];
+      }
+    }
+  }
+  auto activate = [&](int i, auto fc) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < TN; j += GATED ? 2 : 1)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[i][j][v] = act_of<decltype(fc)::value>(acc[i][j][v]);
+  };
+  float* stg = reinterpret_cast<float*>(ring) + wave * 16 * SR;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    switch (P.fn) {
+      case MOE_FN_SILU: activate(i, std::integral_constant<int, MOE_FN_SILU>{}); break;
+      case MOE_FN_GELU_TANH: activate(i, std::integral_constant<int, MOE_FN_GELU_TANH>{}); break;
+      case MOE_FN_GELU_ERF: activate(i, std::integral_constant<int, MOE_FN_GELU_ERF>{}); break;
+      case MOE_FN_RELU: activate(i, std::integral_constant<int, MOE_FN_RELU>{}); break;
+      default: break;
+    }
+#pragma unroll
+    for (int o = 0; o < OC; ++o) {
+      float y[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) y[v] = GATED ? acc[i][2 * o][v] * acc[i][2 * o + 1][v] : acc[i][o][v];
+      *reinterpret_cast<float4*>(stg + r16 * SR + o * 16 + 4 * g) = make_float4(y[0], y[1], y[2], y[3]);
+    }
+    asm volatile("" ::: "memory");  // a wave's LDS accesses keep their order
+#pragma unroll
+    for (int p = 0; p < PS; ++p) {
+      const float4 a = *reinterpret_cast<const float4*>(stg + (p * RP + er) * SR + (lane % LPR) * 8);
+      const float4 b = *reinterpret_cast<const float4*>(stg + (p * RP + er) * SR + (lane % LPR) * 8 + 4);
+      float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      const int t = tw + i * 16 + p * RP + er;
+      if (t < t_end && whole) {
+        if (P.res) {
+          const uint4 q = rr[i % RD][p];
+          const uint32_t d[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[2 * e] += __uint_as_float(d[e] << 16);
+            y[2 * e + 1] += __uint_as_float(d[e] & 0xFFFF0000u);
+          }
+        }
+        const int64_t ob = (int64_t)(tw + i * 16 + p * RP) * P.ldo;  // uniform
+        const uint32_t ol = (uint32_t)(er * (int)P.ldo + ec);
+        if (P.out_f32) {
+          float4* o = reinterpret_cast<float4*>(static_cast<float*>(P.out) + ob + ol);
+          o[0] = make_float4(y[0], y[1], y[2], y[3]);
+          o[1] = make_float4(y[4], y[5], y[6], y[7]);
+        } else {
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.out) + ob + ol) = make_uint4(
+              bf16x2_rne(y[0], y[1]), bf16x2_rne(y[2], y[3]), bf16x2_rne(y[4], y[5]), bf16x2_rne(y[6], y[7]));
+        }
+      } else if (t < t_end) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (ec + e < P.N)
+            put(P, t, ec + e, P.res ? y[e] + bf16_to_f32(P.res[(int64_t)t * P.ldr + ec + e]) : y[e]);
+      }
+    }
+    asm volatile("" ::: "memory");
+    if (i + RD < TM) load_res(i + RD);
+  }
+}
+
 // One output tile a workgroup.
 // WM x WN waves, each TM x TN 16 x 16 tiles; EXACT: E4M3 operands decoded to
 // bf16 (fp32 outputs).  With K split, each tile's run of steps leaves its
@@ -49,7 +169,7 @@ struct LinTiles {
 // MOE_Q_FP8_BLOCK (B: what LinParams does not say): a step is a block of 128
 // columns.  Its matrix instruction starts from zero, and its sums are added to
 // the running ones times the scales' product: 4 FMA beside each instruction,
-// one instruction late so that none waits for its own result.  The step's
+// some instructions late so that none waits for its own result.  The step's
 // scales, the rows' and one of each 16 weight rows, ride in the ring.
 // GROUPED: row tiles of the experts' rows, found from their offsets; the rows
 // of x by index.
@@ -64,9 +184,8 @@ __device__ __forceinline__ void tile_product(LinParams P, const LinTiles& G, con
   constexpr int kScales = RS ? SC * 256 : 0;         // a step's scales, in a ring of S + 1
   constexpr int kWait = (S - 1) * (CA + CB + (RS ? 1 : 0));  // loads of S - 1 steps
   constexpr int TH = TM / 2;
-  constexpr int OC = GATED ? TN / 2 : TN;            // 16-column groups of output a wave
   constexpr int BO = GATED ? BN / 2 : BN;            // output columns a tile
-  constexpr int SR = OC * 16 + 4;                    // staging row, floats
+  constexpr int SR = (GATED ? TN / 2 : TN) * 16 + 4;  // staging row, floats
   static_assert(CA * 8 * NW == BM && CB * 8 * NW == BN && SC <= NW && TN % 2 == 0 && CA % 2 == 0, "tile shape");
   static_assert(!RS || (BM % 64 == 0 && BN % 64 == 0), "whole scale pieces");
   static_assert(!BLK || TN * 16 <= 64, "a wave's weight rows lie in one block");
@@ -243,24 +362,32 @@ __device__ __forceinline__ void tile_product(LinParams P, const LinTiles& G, con
   uint32_t rw[MX ? TN : 1], rx[MX ? TH : 1];                        // MX: scale bytes as read
   uint32_t ew[MX && EXACT ? TN : 1], ex[MX && EXACT ? TM : 1];     // MX, EXACT: the rows' four scales
   float bw[BLK ? 2 : 1], bx[BLK ? TH : 1];  // BLK: scales of the step's weights (gated: gate, up), of the half's rows
-  lf32x4_t late[BLK ? 2 : 1];               // BLK: sums of the last instructions, not added yet
-  float nw[BLK ? 2 : 1], nx[BLK ? TH : 1];  // BLK: those of the next step, of the next half
-  // adds the sums of instruction n of a half
+  float nw[BLK ? 2 : 1], nx[BLK ? TH : 1];  // those of the next step, of the next half
+  // sums of the last instructions, not added yet, and their scales: instruction
+  // n of a half leaves its own in place n % kLate, whose former ones are added first
+  constexpr int kLate = TM > 4 || EXACT ? 2 : 4;
+  lf32x4_t late[BLK ? kLate : 1];
+  float late_f[BLK ? kLate : 1];
+  static_assert(!BLK || TN * TH % kLate == 0, "places go on from half to half");
+  // adds what instruction kLate before number n of half h left (n < kLate: of the other half)
   auto settle = [&](auto nc, auto hc) __attribute__((always_inline)) {
-    constexpr int n = decltype(nc)::value, h = decltype(hc)::value, j = n / TH, i = n % TH;
-    const float f = bx[BLK ? i : 0] * bw[BLK && GATED ? j & 1 : 0];
+    constexpr int N = TN * TH, n = decltype(nc)::value, k = (n + N - kLate) % N;
+    constexpr int h = n < kLate ? 1 - decltype(hc)::value : decltype(hc)::value, j = k / TH, i = h * TH + k % TH;
 #pragma unroll
-    for (int v = 0; v < 4; ++v) acc[h * TH + i][j][v] = fmaf(late[BLK ? n & 1 : 0][v], f, acc[h * TH + i][j][v]);
+    for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(late[n % kLate][v], late_f[n % kLate], acc[i][j][v]);
   };
   auto mma = [&](auto jc, auto ic) __attribute__((always_inline)) {
     constexpr int j = decltype(jc)::value, i = decltype(ic)::value;
     if constexpr (BLK) {
-      constexpr int n = j * TH + i % TH;
+      constexpr int n = j * TH + i % TH, l = n % kLate;
+      settle(std::integral_constant<int, n>{}, std::integral_constant<int, i / TH>{});
+      __builtin_amdgcn_sched_barrier(0);
       lf32x4_t c = lf32x4_t{0.f, 0.f, 0.f, 0.f};
       if constexpr (EXACT) c = mma_decoded<false>(fw[j], fx[i], c, 0, 0, g);
       else c = mma_fp8<0, 0>(fw[j], fx[i], c, 0x7F7F7F7F, 0x7F7F7F7F);
-      late[n & 1] = c;
-      if constexpr (n > 0) settle(std::integral_constant<int, n - 1>{}, std::integral_constant<int, i / TH>{});
+      late[l] = c;
+      late_f[l] = bx[i % TH] * bw[GATED ? j & 1 : 0];
+      __builtin_amdgcn_sched_barrier(0);
       return;
     }
     lf32x4_t c = acc[i][j];
@@ -333,10 +460,9 @@ __device__ __forceinline__ void tile_product(LinParams P, const LinTiles& G, con
     }
     lds_sync();
   };
-  // BLK: the half's last sums; the next half's scales
+  // BLK: the next half's scales
   auto end_half = [&](auto hc) __attribute__((always_inline)) {
     if constexpr (BLK) {
-      settle(std::integral_constant<int, TN * TH - 1>{}, hc);
 #pragma unroll
       for (int i = 0; i < TH; ++i) bx[i] = nx[i];
       if constexpr (decltype(hc)::value == 1) bw[0] = nw[0], bw[1] = nw[1];
@@ -373,6 +499,11 @@ __device__ __forceinline__ void tile_product(LinParams P, const LinTiles& G, con
     bw[0] = nw[0], bw[1] = nw[1];
 #pragma unroll
     for (int i = 0; i < TH; ++i) bx[i] = nx[i];
+#pragma unroll
+    for (int l = 0; l < kLate; ++l) {
+      late[l] = lf32x4_t{0.f, 0.f, 0.f, 0.f};
+      late_f[l] = 0.f;
+    }
   }
   using I0 = std::integral_constant<int, 0>;
   using I1 = std::integral_constant<int, 1>;
@@ -433,6 +564,14 @@ __device__ __forceinline__ void tile_product(LinParams P, const LinTiles& G, con
       sx[0] = pack(rx, TH);
     }
   }
+  if constexpr (BLK) {  // what the last half left
+    settle(I0{}, I0{});
+    settle(std::integral_constant<int, 1>{}, I0{});
+    if constexpr (kLate > 2) {
+      settle(std::integral_constant<int, 2>{}, I0{});
+      settle(std::integral_constant<int, 3>{}, I0{});
+    }
+  }
   // (the largest tile never splits: its grids fill the chip)
   if constexpr (TM * TN <= 16 && !GROUPED) if (G.splits > 1) {
     // the sums as they are, 4 columns a lane
@@ -459,112 +598,7 @@ __device__ __forceinline__ void tile_product(LinParams P, const LinTiles& G, con
     wait_loads<0>();  // no load into LDS outlives the workgroup
     return;
   }
-  // ---- epilogue.  Lane: token r16 of a 16-token group, weight rows 4 g + v
-  // of a group: scales, bias, activation and gate in place; then, through LDS
-  // in fp32, rows of 8 columns a lane: the residual and whole 16-byte stores.
-  constexpr int LPR = OC * 2, RP = 64 / LPR, PS = 16 / RP;  // lanes a row, rows a pass, passes
-  const int er = lane / LPR, ec = n0 + wn * OC * 16 + (lane % LPR) * 8;
-  const int tw = t0 + wm * TM * 16;  // the wave's first token
-  // residual rows, four groups ahead of their stores (out may be the
-  // residual: a lane reads and writes the same places)
-  constexpr int RD = TM < 4 ? TM : 4;
-  uint4 rr[RD][PS];
-  const bool whole = ec + 8 <= P.N && G.vec_out && (G.vec_res || !P.res);
-  auto load_res = [&](int i) __attribute__((always_inline)) {
-    if (P.res && whole) {
-#pragma unroll
-      for (int p = 0; p < PS; ++p) {
-        const int t = tw + i * 16 + p * RP, rows = t_end - t;  // uniform
-        if (rows > 0)
-          rr[i % RD][p] = *reinterpret_cast<const uint4*>(P.res + (int64_t)t * P.ldr +
-                                                          (uint32_t)(min(er, rows - 1) * (int)P.ldr + ec));
-      }
-    }
-  };
-#pragma unroll
-  for (int i = 0; i < RD; ++i) load_res(i);
-  wait_loads<0>();
-  lds_sync();  // nothing reads or fills the ring any more: its memory takes the staging rows
-#pragma unroll
-  for (int j = 0; j < TN; ++j) {
-    const float4 b4 = *reinterpret_cast<const float4*>(s_bias + (wn * TN + j) * 16 + 4 * g);
-    const float bj[4] = {b4.x, b4.y, b4.z, b4.w};
-    float wj[4] = {1.f, 1.f, 1.f, 1.f};
-    if constexpr (QM == MOE_Q_FP8) {
-      const float4 w4 = *reinterpret_cast<const float4*>(s_ws + (wn * TN + j) * 16 + 4 * g);
-      wj[0] = w4.x, wj[1] = w4.y, wj[2] = w4.z, wj[3] = w4.w;
-    }
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      float xs = 1.f;
-      if constexpr (QM == MOE_Q_FP8) xs = s_xs[(wm * TM + i) * 16 + r16];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        if constexpr (QM == MOE_Q_FP8) acc[i][j][v] = fmaf(acc[i][j][v], xs * wj[v], bj[v]);
-        else acc[i][j][v] += bj[v];
-      }
-    }
-  }
-  auto activate = [&](int i, auto fc) __attribute__((always_inline)) {
-#pragma unroll
-    for (int j = 0; j < TN; j += GATED ? 2 : 1)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) acc[i][j][v] = act_of<decltype(fc)::value>(acc[i][j][v]);
-  };
-  float* stg = reinterpret_cast<float*>(ring) + wave * 16 * SR;
-#pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    switch (P.fn) {
-      case MOE_FN_SILU: activate(i, std::integral_constant<int, MOE_FN_SILU>{}); break;
-      case MOE_FN_GELU_TANH: activate(i, std::integral_constant<int, MOE_FN_GELU_TANH>{}); break;
-      case MOE_FN_GELU_ERF: activate(i, std::integral_constant<int, MOE_FN_GELU_ERF>{}); break;
-      case MOE_FN_RELU: activate(i, std::integral_constant<int, MOE_FN_RELU>{}); break;
-      default: break;
-    }
-#pragma unroll
-    for (int o = 0; o < OC; ++o) {
-      float y[4];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) y[v] = GATED ? acc[i][2 * o][v] * acc[i][2 * o + 1][v] : acc[i][o][v];
-      *reinterpret_cast<float4*>(stg + r16 * SR + o * 16 + 4 * g) = make_float4(y[0], y[1], y[2], y[3]);
-    }
-    asm volatile("" ::: "memory");  // a wave's LDS accesses keep their order
-#pragma unroll
-    for (int p = 0; p < PS; ++p) {
-      const float4 a = *reinterpret_cast<const float4*>(stg + (p * RP + er) * SR + (lane % LPR) * 8);
-      const float4 b = *reinterpret_cast<const float4*>(stg + (p * RP + er) * SR + (lane % LPR) * 8 + 4);
-      float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      const int t = tw + i * 16 + p * RP + er;
-      if (t < t_end && whole) {
-        if (P.res) {
-          const uint4 q = rr[i % RD][p];
-          const uint32_t d[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            y[2 * e] += __uint_as_float(d[e] << 16);
-            y[2 * e + 1] += __uint_as_float(d[e] & 0xFFFF0000u);
-          }
-        }
-        const int64_t ob = (int64_t)(tw + i * 16 + p * RP) * P.ldo;  // uniform
-        const uint32_t ol = (uint32_t)(er * (int)P.ldo + ec);
-        if (P.out_f32) {
-          float4* o = reinterpret_cast<float4*>(static_cast<float*>(P.out) + ob + ol);
-          o[0] = make_float4(y[0], y[1], y[2], y[3]);
-          o[1] = make_float4(y[4], y[5], y[6], y[7]);
-        } else {
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.out) + ob + ol) = make_uint4(
-              bf16x2_rne(y[0], y[1]), bf16x2_rne(y[2], y[3]), bf16x2_rne(y[4], y[5]), bf16x2_rne(y[6], y[7]));
-        }
-      } else if (t < t_end) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (ec + e < P.N)
-            put(P, t, ec + e, P.res ? y[e] + bf16_to_f32(P.res[(int64_t)t * P.ldr + ec + e]) : y[e]);
-      }
-    }
-    asm volatile("" ::: "memory");
-    if (i + RD < TM) load_res(i + RD);
-  }
+  tile_epilogue<QM, GATED, WM, WN, TM, TN>(P, G, acc, ring, s_bias, s_ws, s_xs, t0, t_end, n0);
 }
 
 // The tiles of the linear product (linear_tile.hip).
