@@ -97,6 +97,9 @@ bool block_tile_fits(const BlockParams& B);
 void launch_block_tile(const BlockParams& B, const TilePlan& pl, void* workspace, hipStream_t s);
 // Tiles of 256 x 256 (linear_block_big.hip): bf16 outputs, K not split.
 void launch_block_big(const BlockParams& B, hipStream_t s);
+// Tiles of 128 x 128 walked by two workgroups a CU (linear_block_stream.hip):
+// bf16 outputs, K not split and at least two blocks, at most kStreamTiles tiles a workgroup.
+void launch_block_stream(const BlockParams& B, hipStream_t s);
 
 size_t linear_block_workspace(int T, int N, int K, bool gated, bool out_f32);
 void launch_linear_block(const BlockParams& B, void* workspace, hipStream_t s);

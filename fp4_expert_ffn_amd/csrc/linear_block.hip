@@ -138,7 +138,7 @@ namespace moe {
 size_t linear_block_workspace(int T, int N, int K, bool gated, bool out_f32) {
   const int R = gated ? 2 * N : N;
   if (block_small_wins(T, R, gated, K, out_f32)) return 0;
-  const TilePlan pl = plan_block_tiles(T, R, K, out_f32);
+  const TilePlan pl = plan_block_tiles(T, N, gated, K, out_f32);
   return pl.splits > 1 ? (size_t)pl.splits * T * R * sizeof(float) : 0;
 }
 
@@ -147,10 +147,11 @@ void launch_linear_block(const BlockParams& B, void* workspace, hipStream_t s) {
   const bool fits = block_tile_fits(B);
   if (B.offsets) {
     if (!fits || grouped_small_wins(P.T, B.E)) launch_small<true>(B, s);
-    else launch_block_tile(B, plan_grouped_tiles(P.T, B.E, P.K, P.out_f32), nullptr, s);
+    else launch_block_tile(B, plan_grouped_tiles(P.T, B.E, P.N, P.gated, P.K, P.out_f32, most_row_blocks(P.T, B.E, 128)),
+                           nullptr, s);
   } else {
     if (!fits || block_small_wins(P.T, P.R, P.gated, P.K, P.out_f32)) launch_small<false>(B, s);
-    else launch_block_tile(B, plan_block_tiles(P.T, P.R, P.K, P.out_f32), workspace, s);
+    else launch_block_tile(B, plan_block_tiles(P.T, P.N, P.gated, P.K, P.out_f32), workspace, s);
   }
 }
 

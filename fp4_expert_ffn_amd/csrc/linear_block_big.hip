@@ -13,18 +13,19 @@
 //   - fragments of x are read two parts ahead, four in registers; those of the
 //     next step's weights as the last part uses up this one's.
 //   - after part 0 every wave has the step's weights in registers: their
-//     place takes the weights of step s + 2 (loads in parts 1 to 4).  Before
-//     part 6 every wave has read the step's rows of x: their place takes those
-//     of step s + 2 (parts 6 and 7), and the same barrier says that step s + 1
-//     has landed.
-// So a load has a step (x) or a step and a half (weights) to land in two
-// stages, and each barrier stands where no wave waits for its own reads.
+//     place takes the weights of step s + 2 (parts 2 to 5).  Before part 6
+//     every wave has read the step's rows of x: their place takes those of step
+//     s + 2 (parts 6 and 7, and 0 and 1 of the next step), and the same barrier
+//     says that step s + 1 has landed.
+// So a load has from five parts to a step and a half to land in two stages,
+// the loads go out evenly, and each barrier stands where no wave waits for its
+// own reads.
 #include <algorithm>
 #include <type_traits>
 
 #include "linear_block.h"
+#include "linear_block_epilogue.h"
 #include "linear_block_plan.h"
-#include "linear_tile.h"
 
 namespace moe {
 
@@ -38,7 +39,6 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   constexpr uint32_t kScales = 5 * 256;                      // a step's scales: 256 rows, 16 groups of weight rows
   __shared__ __align__(1024) uint8_t ring[2 * kStage];
   __shared__ __align__(256) uint8_t s_sc[3 * kScales];
-  __shared__ __align__(16) float s_bias[BN];
   LinParams P = B.L;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN, r16 = lane & 15, g = lane >> 4, lr = lane >> 3;
@@ -123,10 +123,14 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
     for (int u = 0; u < 4; ++u) load_w(u);
     next_w();
-#pragma unroll
-    for (int u = 0; u < 4; ++u) load_x(u);
-    load_s();
-    next_x();
+    load_x(0);
+    load_x(1);
+    if (s == 0) {  // the rest of step 1's: in step 0
+      load_x(2);
+      load_x(3);
+      load_s();
+      next_x();
+    }
   }
   // ---- compute side
   lf32x4_t acc[TM][TN], late[TN];
@@ -154,7 +158,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     fx[i & 3].b = *reinterpret_cast<const uint4*>(ring + st + (rda ^ 64) + i * 2048);
     bx[i & 3] = *reinterpret_cast<const float*>(s_sc + sp + rsa + i * 64);
   };
-  wait_loads<9>();  // step 0
+  wait_loads<6>();  // step 0
   lds_sync();
 #pragma unroll
   for (int j = 0; j < TN; ++j) read_w(0, 0, j);
@@ -183,23 +187,21 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         late[j] = mma_fp8<0, 0>(fw[j], fx[i & 3], lf32x4_t{0.f, 0.f, 0.f, 0.f}, 0x7F7F7F7F, 0x7F7F7F7F);
         late_f[j] = bx[i & 3] * bw[GATED ? j & 1 : 0];
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (i >= 1 && i <= 4) {
-          if (j == 1) load_w(i - 1);
+        // one load a part: together they would hold back every wave's instructions behind the texture unit
+        if (j == 1) {
+          if constexpr (i < 2) load_x(i + 2);
+          else if constexpr (i < 6) load_w(i - 2);
+          else load_x(i - 6);
         }
-        if constexpr (i == 6) {
-          if (j == 0) load_x(0);
-          if (j == 2) load_x(1);
+        if constexpr (i == 1) {
           if (j == 3) load_s();
         }
-        if constexpr (i == 7) {
-          if (j == 0) load_x(2);
-          if (j == 2) load_x(3);
-          read_w(nx, nsp, j);
-        }
+        if constexpr (i == 7) read_w(nx, nsp, j);
         __builtin_amdgcn_sched_barrier(0);
       }
       if constexpr (i == 0) lds_sync();  // every wave has the step's weights
-      if constexpr (i == 4) next_w();
+      if constexpr (i == 1) next_x();
+      if constexpr (i == 5) next_w();
     };
     part(std::integral_constant<int, 0>{});
     part(std::integral_constant<int, 1>{});
@@ -209,7 +211,6 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     part(std::integral_constant<int, 5>{});
     part(std::integral_constant<int, 6>{});
     part(std::integral_constant<int, 7>{});
-    next_x();
     bw[0] = nw[0];
     bw[1] = nw[1];
     at = nx;
@@ -219,11 +220,10 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   for (int j = 0; j < TN; ++j)
 #pragma unroll
     for (int v = 0; v < 4; ++v) acc[TM - 1][j][v] = fmaf(late[j][v], late_f[j], acc[TM - 1][j][v]);
-  if (tid < BN) {
-    const int col = min(n0 + (GATED ? (tid >> 5) * 16 + (tid & 15) : tid), P.N - 1) + (GATED && ((tid >> 4) & 1) ? P.N : 0);
-    s_bias[tid] = P.bias ? P.bias[col] : 0.f;
-  }
-  tile_epilogue<MOE_Q_FP8_BLOCK, GATED, WM, WN, TM, TN>(P, G, acc, ring, s_bias, nullptr, nullptr, t0, t_end, n0);
+  wait_loads<0>();
+  lds_sync();  // nothing reads or fills the ring any more: its memory takes the staging rows
+  block_epilogue<GATED, WM, WN, TM, TN, GATED ? TN / 2 : TN>(P, G, acc, reinterpret_cast<float*>(ring), t0, t_end, n0, lane,
+                                                             wave);
 }
 
 template <bool GATED, bool GROUPED>

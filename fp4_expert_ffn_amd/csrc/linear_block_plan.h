@@ -9,27 +9,44 @@
 
 namespace moe {
 
+constexpr int kStreamTiles = 128;  // tiles a workgroup of k_block_stream holds
+// Shapes beside kShapes[2 ..], which k_block_tile takes.
+constexpr int kBig = 0;     // k_block_big
+constexpr int kStream = 5;  // k_block_stream
+
 // Whether k_block_small takes the dense call.
 inline bool block_small_wins(int T, int R, bool gated, int K, bool exact) { return small_wins(T, R, gated, K, exact); }
 
-// Tiles of 256 x 256 where they fill the chip, else of 128 x 128, two a CU
-// (4096 x 4096 x 7168: 100 against 121 us; 4096 x 7168 x 2048 67 against 72; 1024 x 4096 x 2048 29
-// against 16).
-inline TilePlan plan_block_tiles(int T, int R, int K, bool exact) {
-  const long long big = (long long)((T + 255) / 256) * ((R + 255) / 256);
-  if (!exact && big >= 192) return TilePlan{0, 1, K / 128};
+// 256 x 256 tiles where they fill the chip, else the shapes of the linear
+// product from 128 x 128 on, K split where that helps.  128 x 128 tiles that
+// pass two a CU are walked without a pause.  us, 256 x 256, walked, 128 x 128:
+// 4096 x 4096 x 7168 102, 121, 126; 4096 x 7168 x 2048 64, 66, 72; 1024 x 4096
+// x 2048 29, 15.6, 16.4.  fp32 outputs (exact): k_block_tile alone.
+inline TilePlan plan_block_tiles(int T, int N, bool gated, int K, bool exact) {
+  const int R = gated ? 2 * N : N, steps = K / 128;
+  const int64_t big = (int64_t)((T + 255) / 256) * (gated ? (N + 127) / 128 : (N + 255) / 256);
+  if (!exact && big >= 192) return TilePlan{kBig, 1, steps};
   TilePlan pl = plan_tiles(T, R, K, exact);
-  if (pl.shape < 2) pl.shape = 2;
+  pl.shape = std::max(pl.shape, 2);
+  const int64_t tiles = (int64_t)((T + 127) / 128) * (gated ? (N + 63) / 64 : (N + 127) / 128);
+  if (!exact && steps >= 2 && tiles > 2 * kCus && tiles <= (int64_t)2 * kCus * kStreamTiles) return TilePlan{kStream, 1, steps};
   return pl;
 }
 
-// Grouped: rows a workgroup by the mean number of an expert's rows.
+// Grouped: k_block_small while the experts have few rows each.
 inline bool grouped_small_wins(int T, int E) { return T <= 16 * E; }
 
-inline TilePlan plan_grouped_tiles(int T, int E, int K, bool exact) {
-  const int mean = T / E, steps = K / 128;
-  const int shape = mean >= 32 ? 2 : 3;
-  return TilePlan{shape, 1, steps};
+// Else tiles walked without a pause: where the experts start and end is known
+// on the device alone, and each tile's look for its own place, its first loads
+// and its epilogue would stand still a CU's half.  us, 4096 tokens by 8 of 128
+// experts: 2 x 768 x 2048 180 against 207 with a workgroup a tile, 2048 x 768
+// 112 against 149; 512 tokens, 2 x 768 x 2048 93 against 97 (64 x 128 tiles).
+// most: the most row blocks of 128 there can be.
+inline TilePlan plan_grouped_tiles(int T, int E, int N, bool gated, int K, bool exact, int64_t most) {
+  const int steps = K / 128;
+  const int64_t tiles = most * (gated ? (N + 63) / 64 : (N + 127) / 128);
+  if (!exact && steps >= 2 && tiles <= (int64_t)2 * kCus * kStreamTiles) return TilePlan{kStream, 1, steps};
+  return TilePlan{T / E >= 48 ? 2 : 3, 1, steps};
 }
 
 }  // namespace moe

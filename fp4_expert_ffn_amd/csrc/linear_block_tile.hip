@@ -1,6 +1,8 @@
 // The FP8 product with a scale per block of 128 for batches: the linear
 // product's tiles (linear_tile.h) with the scales of each 128-column step in
-// the ring, dense and over the row tiles of routed experts.
+// the ring, dense and over the row tiles of routed experts.  fp32 outputs, K
+// split and small grids; longer batches: linear_block_big.hip and
+// linear_block_stream.hip.
 #include <algorithm>
 
 #include "linear_block.h"
@@ -10,9 +12,9 @@
 namespace moe {
 
 bool block_tile_fits(const BlockParams& B) {
-  // 32-bit offsets inside a tile's rows; grouped: over all of x
+  // 32-bit offsets inside a tile's rows (grouped: over all of x) and over the weights' scales
   constexpr int64_t lim = 1 << 24;
-  return B.L.ldx < lim && B.L.ldw < lim && B.L.ldr < lim && B.L.ldo < lim;
+  return B.L.ldx < lim && B.L.ldw < lim && B.L.ldr < lim && B.L.ldo < lim && (int64_t)B.nb * B.steps < (1 << 28);
 }
 
 namespace {
@@ -40,8 +42,7 @@ void launch_one(const BlockParams& B, const TilePlan& pl, float* part, hipStream
 
 template <bool GATED, bool EXACT, bool GROUPED>
 void launch_shape(const BlockParams& B, const TilePlan& pl, float* part, hipStream_t s) {
-  if (pl.shape == 1) launch_one<GATED, EXACT, GROUPED, 2, 4, 4, 4, 3>(B, pl, part, s);
-  else if (pl.shape == 2) launch_one<GATED, EXACT, GROUPED, 2, 2, 4, 4, 2>(B, pl, part, s);
+  if (pl.shape == 2) launch_one<GATED, EXACT, GROUPED, 2, 2, 4, 4, 2>(B, pl, part, s);
   else if (pl.shape == 3) launch_one<GATED, EXACT, GROUPED, 2, 2, 2, 4, 3>(B, pl, part, s);
   else launch_one<GATED, EXACT, GROUPED, 2, 1, 2, 4, 3>(B, pl, part, s);
 }
@@ -56,7 +57,8 @@ void launch_out(const BlockParams& B, const TilePlan& pl, float* part, hipStream
 
 void launch_block_tile(const BlockParams& B, const TilePlan& pl, void* workspace, hipStream_t s) {
   float* part = static_cast<float*>(workspace);
-  if (pl.shape == 0) return launch_block_big(B, s);
+  if (pl.shape == kBig) return launch_block_big(B, s);
+  if (pl.shape == kStream) return launch_block_stream(B, s);
   if (B.offsets) B.L.gated ? launch_out<true, true>(B, pl, part, s) : launch_out<false, true>(B, pl, part, s);
   else B.L.gated ? launch_out<true, false>(B, pl, part, s) : launch_out<false, false>(B, pl, part, s);
 }

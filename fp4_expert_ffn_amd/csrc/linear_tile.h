@@ -41,126 +41,6 @@ struct LinTiles {
   float* part;           // splits > 1: the sums [splits][T][R]
 };
 
-// The epilogue of a tile from its sums: rows t0 .. t_end - 1 at most, output
-// columns from n0 on; bias and, MOE_Q_FP8, row scales in LDS; ring: LDS that
-// nothing reads or fills any more, 16 rows of SR floats a wave.
-template <int QM, bool GATED, int WM, int WN, int TM, int TN>
-__device__ __forceinline__ void tile_epilogue(const LinParams& P, const LinTiles& G, lf32x4_t (&acc)[TM][TN], uint8_t* ring,
-                                              const float* s_bias, const float* s_ws, const float* s_xs, int t0, int t_end,
-                                              int n0) {
-  constexpr int OC = GATED ? TN / 2 : TN;            // 16-column groups of output a wave
-  constexpr int SR = OC * 16 + 4;                    // staging row, floats
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / WN, wn = wave % WN;
-  const int r16 = lane & 15, g = lane >> 4;
-  // ---- epilogue.  Lane: token r16 of a 16-token group, weight rows 4 g + v
-  // of a group: scales, bias, activation and gate in place; then, through LDS
-  // in fp32, rows of 8 columns a lane: the residual and whole 16-byte stores.
-  constexpr int LPR = OC * 2, RP = 64 / LPR, PS = 16 / RP;  // lanes a row, rows a pass, passes
-  const int er = lane / LPR, ec = n0 + wn * OC * 16 + (lane % LPR) * 8;
-  const int tw = t0 + wm * TM * 16;  // the wave's first token
-  // residual rows, four groups ahead of their stores (out may be the
-  // residual: a lane reads and writes the same places)
-  constexpr int RD = TM < 4 ? TM : 4;
-  uint4 rr[RD][PS];
-  const bool whole = ec + 8 <= P.N && G.vec_out && (G.vec_res || !P.res);
-  auto load_res = [&](int i) __attribute__((always_inline)) {
-    if (P.res && whole) {
-#pragma unroll
-      for (int p = 0; p < PS; ++p) {
-        const int t = tw + i * 16 + p * RP, rows = t_end - t;  // uniform
-        if (rows > 0)
-          rr[i % RD][p] = *reinterpret_cast<const uint4*>(P.res + (int64_t)t * P.ldr +
-                                                          (uint32_t)(min(er, rows - 1) * (int)P.ldr + ec));
-      }
-    }
-  };
-#pragma unroll
-  for (int i = 0; i < RD; ++i) load_res(i);
-  wait_loads<0>();
-  lds_sync();  // nothing reads or fills the ring any more: its memory takes the staging rows
-#pragma unroll
-  for (int j = 0; j < TN; ++j) {
-    const float4 b4 = *reinterpret_cast<const float4*>(s_bias + (wn * TN + j) * 16 + 4 * g);
-    const float bj[4] = {b4.x, b4.y, b4.z, b4.w};
-    float wj[4] = {1.f, 1.f, 1.f, 1.f};
-    if constexpr (QM == MOE_Q_FP8) {
-      const float4 w4 = *reinterpret_cast<const float4*>(s_ws + (wn * TN + j) * 16 + 4 * g);
-      wj[0] = w4.x, wj[1] = w4.y, wj[2] = w4.z, wj[3] = w4.w;
-    }
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      float xs = 1.f;
-      if constexpr (QM == MOE_Q_FP8) xs = s_xs[(wm * TM + i) * 16 + r16];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        if constexpr (QM == MOE_Q_FP8) acc[i][j][v] = fmaf(acc[i][j][v], xs * wj[v], bj[v]);
-        else acc[i][j][v] += bj[v];
-      }
-    }
-  }
-  auto activate = [&](int i, auto fc) __attribute__((always_inline)) {
-#pragma unroll
-    for (int j = 0; j < TN; j += GATED ? 2 : 1)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) acc[i][j][v] = act_of<decltype(fc)::value>(acc[i][j][v]);
-  };
-  float* stg = reinterpret_cast<float*>(ring) + wave * 16 * SR;
-#pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    switch (P.fn) {
-      case MOE_FN_SILU: activate(i, std::integral_constant<int, MOE_FN_SILU>{}); break;
-      case MOE_FN_GELU_TANH: activate(i, std::integral_constant<int, MOE_FN_GELU_TANH>{}); break;
-      case MOE_FN_GELU_ERF: activate(i, std::integral_constant<int, MOE_FN_GELU_ERF>{}); break;
-      case MOE_FN_RELU: activate(i, std::integral_constant<int, MOE_FN_RELU>{}); break;
-      default: break;
-    }
-#pragma unroll
-    for (int o = 0; o < OC; ++o) {
-      float y[4];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) y[v] = GATED ? acc[i][2 * o][v] * acc[i][2 * o + 1][v] : acc[i][o][v];
-      *reinterpret_cast<float4*>(stg + r16 * SR + o * 16 + 4 * g) = make_float4(y[0], y[1], y[2], y[3]);
-    }
-    asm volatile("" ::: "memory");  // a wave's LDS accesses keep their order
-#pragma unroll
-    for (int p = 0; p < PS; ++p) {
-      const float4 a = *reinterpret_cast<const float4*>(stg + (p * RP + er) * SR + (lane % LPR) * 8);
-      const float4 b = *reinterpret_cast<const float4*>(stg + (p * RP + er) * SR + (lane % LPR) * 8 + 4);
-      float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      const int t = tw + i * 16 + p * RP + er;
-      if (t < t_end && whole) {
-        if (P.res) {
-          const uint4 q = rr[i % RD][p];
-          const uint32_t d[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            y[2 * e] += __uint_as_float(d[e] << 16);
-            y[2 * e + 1] += __uint_as_float(d[e] & 0xFFFF0000u);
-          }
-        }
-        const int64_t ob = (int64_t)(tw + i * 16 + p * RP) * P.ldo;  // uniform
-        const uint32_t ol = (uint32_t)(er * (int)P.ldo + ec);
-        if (P.out_f32) {
-          float4* o = reinterpret_cast<float4*>(static_cast<float*>(P.out) + ob + ol);
-          o[0] = make_float4(y[0], y[1], y[2], y[3]);
-          o[1] = make_float4(y[4], y[5], y[6], y[7]);
-        } else {
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.out) + ob + ol) = make_uint4(
-              bf16x2_rne(y[0], y[1]), bf16x2_rne(y[2], y[3]), bf16x2_rne(y[4], y[5]), bf16x2_rne(y[6], y[7]));
-        }
-      } else if (t < t_end) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (ec + e < P.N)
-            put(P, t, ec + e, P.res ? y[e] + bf16_to_f32(P.res[(int64_t)t * P.ldr + ec + e]) : y[e]);
-      }
-    }
-    asm volatile("" ::: "memory");
-    if (i + RD < TM) load_res(i + RD);
-  }
-}
-
 // One output tile a workgroup.
 // WM x WN waves, each TM x TN 16 x 16 tiles; EXACT: E4M3 operands decoded to
 // bf16 (fp32 outputs).  With K split, each tile's run of steps leaves its
@@ -184,8 +64,9 @@ __device__ __forceinline__ void tile_product(LinParams P, const LinTiles& G, con
   constexpr int kScales = RS ? SC * 256 : 0;         // a step's scales, in a ring of S + 1
   constexpr int kWait = (S - 1) * (CA + CB + (RS ? 1 : 0));  // loads of S - 1 steps
   constexpr int TH = TM / 2;
+  constexpr int OC = GATED ? TN / 2 : TN;            // 16-column groups of output a wave
   constexpr int BO = GATED ? BN / 2 : BN;            // output columns a tile
-  constexpr int SR = (GATED ? TN / 2 : TN) * 16 + 4;  // staging row, floats
+  constexpr int SR = OC * 16 + 4;                    // staging row, floats
   static_assert(CA * 8 * NW == BM && CB * 8 * NW == BN && SC <= NW && TN % 2 == 0 && CA % 2 == 0, "tile shape");
   static_assert(!RS || (BM % 64 == 0 && BN % 64 == 0), "whole scale pieces");
   static_assert(!BLK || TN * 16 <= 64, "a wave's weight rows lie in one block");
@@ -598,7 +479,112 @@ __device__ __forceinline__ void tile_product(LinParams P, const LinTiles& G, con
     wait_loads<0>();  // no load into LDS outlives the workgroup
     return;
   }
-  tile_epilogue<QM, GATED, WM, WN, TM, TN>(P, G, acc, ring, s_bias, s_ws, s_xs, t0, t_end, n0);
+  // ---- epilogue.  Lane: token r16 of a 16-token group, weight rows 4 g + v
+  // of a group: scales, bias, activation and gate in place; then, through LDS
+  // in fp32, rows of 8 columns a lane: the residual and whole 16-byte stores.
+  constexpr int LPR = OC * 2, RP = 64 / LPR, PS = 16 / RP;  // lanes a row, rows a pass, passes
+  const int er = lane / LPR, ec = n0 + wn * OC * 16 + (lane % LPR) * 8;
+  const int tw = t0 + wm * TM * 16;  // the wave's first token
+  // residual rows, four groups ahead of their stores (out may be the
+  // residual: a lane reads and writes the same places)
+  constexpr int RD = TM < 4 ? TM : 4;
+  uint4 rr[RD][PS];
+  const bool whole = ec + 8 <= P.N && G.vec_out && (G.vec_res || !P.res);
+  auto load_res = [&](int i) __attribute__((always_inline)) {
+    if (P.res && whole) {
+#pragma unroll
+      for (int p = 0; p < PS; ++p) {
+        const int t = tw + i * 16 + p * RP, rows = t_end - t;  // uniform
+        if (rows > 0)
+          rr[i % RD][p] = *reinterpret_cast<const uint4*>(P.res + (int64_t)t * P.ldr +
+                                                          (uint32_t)(min(er, rows - 1) * (int)P.ldr + ec));
+      }
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < RD; ++i) load_res(i);
+  wait_loads<0>();
+  lds_sync();  // nothing reads or fills the ring any more: its memory takes the staging rows
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+    const float4 b4 = *reinterpret_cast<const float4*>(s_bias + (wn * TN + j) * 16 + 4 * g);
+    const float bj[4] = {b4.x, b4.y, b4.z, b4.w};
+    float wj[4] = {1.f, 1.f, 1.f, 1.f};
+    if constexpr (QM == MOE_Q_FP8) {
+      const float4 w4 = *reinterpret_cast<const float4*>(s_ws + (wn * TN + j) * 16 + 4 * g);
+      wj[0] = w4.x, wj[1] = w4.y, wj[2] = w4.z, wj[3] = w4.w;
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      float xs = 1.f;
+      if constexpr (QM == MOE_Q_FP8) xs = s_xs[(wm * TM + i) * 16 + r16];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        if constexpr (QM == MOE_Q_FP8) acc[i][j][v] = fmaf(acc[i][j][v], xs * wj[v], bj[v]);
+        else acc[i][j][v] += bj[v];
+      }
+    }
+  }
+  auto activate = [&](int i, auto fc) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < TN; j += GATED ? 2 : 1)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[i][j][v] = act_of<decltype(fc)::value>(acc[i][j][v]);
+  };
+  float* stg = reinterpret_cast<float*>(ring) + wave * 16 * SR;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    switch (P.fn) {
+      case MOE_FN_SILU: activate(i, std::integral_constant<int, MOE_FN_SILU>{}); break;
+      case MOE_FN_GELU_TANH: activate(i, std::integral_constant<int, MOE_FN_GELU_TANH>{}); break;
+      case MOE_FN_GELU_ERF: activate(i, std::integral_constant<int, MOE_FN_GELU_ERF>{}); break;
+      case MOE_FN_RELU: activate(i, std::integral_constant<int, MOE_FN_RELU>{}); break;
+      default: break;
+    }
+#pragma unroll
+    for (int o = 0; o < OC; ++o) {
+      float y[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) y[v] = GATED ? acc[i][2 * o][v] * acc[i][2 * o + 1][v] : acc[i][o][v];
+      *reinterpret_cast<float4*>(stg + r16 * SR + o * 16 + 4 * g) = make_float4(y[0], y[1], y[2], y[3]);
+    }
+    asm volatile("" ::: "memory");  // a wave's LDS accesses keep their order
+#pragma unroll
+    for (int p = 0; p < PS; ++p) {
+      const float4 a = *reinterpret_cast<const float4*>(stg + (p * RP + er) * SR + (lane % LPR) * 8);
+      const float4 b = *reinterpret_cast<const float4*>(stg + (p * RP + er) * SR + (lane % LPR) * 8 + 4);
+      float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      const int t = tw + i * 16 + p * RP + er;
+      if (t < t_end && whole) {
+        if (P.res) {
+          const uint4 q = rr[i % RD][p];
+          const uint32_t d[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[2 * e] += __uint_as_float(d[e] << 16);
+            y[2 * e + 1] += __uint_as_float(d[e] & 0xFFFF0000u);
+          }
+        }
+        const int64_t ob = (int64_t)(tw + i * 16 + p * RP) * P.ldo;  // uniform
+        const uint32_t ol = (uint32_t)(er * (int)P.ldo + ec);
+        if (P.out_f32) {
+          float4* o = reinterpret_cast<float4*>(static_cast<float*>(P.out) + ob + ol);
+          o[0] = make_float4(y[0], y[1], y[2], y[3]);
+          o[1] = make_float4(y[4], y[5], y[6], y[7]);
+        } else {
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.out) + ob + ol) = make_uint4(
+              bf16x2_rne(y[0], y[1]), bf16x2_rne(y[2], y[3]), bf16x2_rne(y[4], y[5]), bf16x2_rne(y[6], y[7]));
+        }
+      } else if (t < t_end) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (ec + e < P.N)
+            put(P, t, ec + e, P.res ? y[e] + bf16_to_f32(P.res[(int64_t)t * P.ldr + ec + e]) : y[e]);
+      }
+    }
+    asm volatile("" ::: "memory");
+    if (i + RD < TM) load_res(i + RD);
+  }
 }
 
 // The tiles of the linear product (linear_tile.hip).
