@@ -1,21 +1,28 @@
 // Log probabilities of given tokens, their ranks, the rows' entropies and the
 // k most likely tokens, in one read of the logits (gfx950, wave64).
 //
-// With z = scale * l, m the row's largest logit and d_i = scale * (l_i - m):
+// With m the row's largest logit l, c = scale * log2(e) and d_i = c (l_i - m):
 //
-//   s0 = sum exp(d_i), s1 = sum d_i exp(d_i)
-//   lse = scale * m + log s0, log p_i = d_i - log s0, entropy = log s0 - s1 / s0
+//   s0 = sum 2^d_i, s1 = sum d_i 2^d_i
+//   log p_i = scale (l_i - m) - ln s0,  lse = scale m + ln s0,
+//   entropy = ln s0 - ln 2 s1 / s0
 //
-// A thread keeps its own maximum and sums over what it reads and rescales
-// them when the maximum grows; threads, waves and the pieces of a row are
-// joined the same way, in 64 bits.  The k best are keys of 64 bits (the
-// logit's order, then the lower id), which a wave holds sorted over its lanes:
-// logits that pass its k-th best are gathered in LDS, and every 64 of them are
-// sorted and merged into the list, so that no order of the logits costs more
-// than one sort per 64.
+// A thread takes its sums against b, the rounded c times its own maximum, so
+// that an exponent is one FMA, and rescales them when the maximum grows.
+// Threads, waves and the pieces of a row are joined the same way, in 64 bits,
+// and b - c m is put back there: the largest logit counts as exactly 1.
 //
-// Few rows are cut into pieces of one workgroup each, joined by a second
-// kernel.
+// The k best are keys of 64 bits (the logit's order, then the lower id), which
+// a wave holds sorted over its lanes.  What passes the bar (the best k-th best
+// of the workgroup's waves; at first the k-th best of the lanes' largest) is
+// gathered in LDS, and every 64 of them are sorted and merged into the list:
+// no order of the logits costs more than one sort per 64.
+//
+// Ranks are counted by ballots, on the scalar unit, and only where some lane's
+// largest reaches the given logit.
+//
+// Rows whose c m is beyond 1e8, infinite ones among them, or that hold a NaN,
+// are summed once more, in 64 bits (finish_row).
 #include <algorithm>
 
 #include "common.h"
@@ -45,12 +52,12 @@ struct LogprobParams {
   uint8_t* ws;        // splits > 1: [T * splits] Piece, then [T * splits][k] keys
 };
 
-// What a piece of a row leaves: its maximum, the two sums in base 2 (s1 of
-// log2(e) d), and the tokens in front of the given one.
+// What a piece of a row leaves: its maximum, the two sums against b, and the
+// tokens in front of the given one.
 struct Piece {
   double s0, s1;
-  float m;
-  int rank;
+  float m, b;
+  int rank, pad;
 };
 
 // The order of tokens as one number: the logit's order (equal values equal,
@@ -144,13 +151,10 @@ __device__ __forceinline__ float wave_max(float v) {
   return max_rows4(v);
 }
 
-// Sums taken against maximum m as sums against a larger one (c: log2(e) scale).
-template <typename F>
-__device__ __forceinline__ void rebase(F& s0, F& s1, float m, float to, float c) {
-  if (m == to) return;
-  const F d = m == -__builtin_inff() ? (F)-2000 : (F)(m - to) * (F)c;  // nothing below: sums of 0
-  const F f = (F)exp2((F)(d < (F)-1000 ? (F)-1000 : d));
-  s1 = f * (s1 + (d < (F)-1000 ? (F)0 : d) * s0);
+// Sums taken against b as sums against `to`.
+__device__ __forceinline__ void rebase(double& s0, double& s1, double b, double to) {
+  const double d = fmax(b - to, -1000.0), f = exp2(d);
+  s1 = f * (s1 + d * s0);
   s0 = f * s0;
 }
 
@@ -159,44 +163,57 @@ __device__ __forceinline__ float logit(const void* row, int i) {
   return F32 ? static_cast<const float*>(row)[i] : bf16_to_f32(static_cast<const uint16_t*>(row)[i]);
 }
 
-// A row whose largest logit is infinite (nothing but -inf, or +inf among
-// them), or that has a NaN logit (s0 is NaN then, as with +inf): the tokens
-// equal to the maximum share it, and `nan` says whether there is a NaN.
-template <bool F32>
-__device__ void count_equal(const LogprobParams& P, const void* row, float m, int tid, int* s_equal, int* s_nan) {
-  int n = 0, bad = 0;
-  for (int i = tid; i < P.V; i += kThreads) {
-    const float v = logit<F32>(row, i);
-    n += v == m;
-    bad |= v != v;
-  }
-  if (n) atomicAdd(s_equal, n);
-  if (bad) atomicOr(s_nan, 1);
-}
+// b, rounded, is off by up to 2^-24 |c m|: 2^(c m - b), which the joins put
+// back, stays small below 1e8.  kLeast: b of what has seen no c l above it.
+constexpr float kHuge = 1e8f, kLeast = -1e8f;
 
-// The outputs of a row from its joined sums, by the whole workgroup: lane l
-// of wave 0 holds the l-th best key.
-template <bool F32>
-__device__ __forceinline__ void finish_row(const LogprobParams& P, int t, const void* row, float m, double s0, double s1,
-                                           int rank, uint64_t best) {
-  __shared__ int s_equal, s_nan;
+// The outputs of a row from its joined sums against b, by the whole workgroup
+// of NT threads: lane l of wave 0 holds the l-th best key.
+template <bool F32, int NT>
+__device__ __forceinline__ void finish_row(const LogprobParams& P, int t, const void* row, float m, float b, double s0,
+                                           double s1, int rank, uint64_t best) {
+  __shared__ double s_sum[NT / 64][2];
+  __shared__ int s_nan;
   const int tid = threadIdx.x;
-  const bool odd = !(fabsf(m) < __builtin_inff()) || s0 != s0;
+  const bool endless = !(fabsf(m) < __builtin_inff());
+  const double mc = (double)m * (double)P.c;
+  const bool odd = !(fabs(mc) < (double)kHuge) || s0 != s0;
   bool nan = false;
-  if (odd) {  // uniform
-    if (tid == 0) s_equal = s_nan = 0;
+  if (!odd) {
+    rebase(s0, s1, b, mc);
+  } else {  // uniform: the sums once more.  An endless m: tokens equal to it share the row
+    if (tid == 0) s_nan = 0;
     __syncthreads();
-    count_equal<F32>(P, row, m, tid, &s_equal, &s_nan);
+    double a0 = 0, a1 = 0;
+    bool bad = false;
+    for (int i = tid; i < P.V; i += NT) {
+      const float v = logit<F32>(row, i);
+      bad = bad || v != v;
+      const double d = v == m ? 0.0 : (endless ? -2000.0 : fmax((double)P.c * (double)v - mc, -2000.0));
+      const double e = d <= -2000.0 ? 0.0 : exp2(d);
+      a0 += e;
+      a1 += d * e;
+    }
+    if (bad) atomicOr(&s_nan, 1);
+    a0 = wave_sum64(a0);
+    a1 = wave_sum64(a1);
+    if ((tid & 63) == 0) {
+      s_sum[tid >> 6][0] = a0;
+      s_sum[tid >> 6][1] = a1;
+    }
     __syncthreads();
     nan = s_nan != 0;
-    s0 = s_equal;
-    s1 = 0;
+    s0 = s1 = 0;
+    for (int w = 0; w < NT / 64; ++w) {
+      s0 += s_sum[w][0];
+      s1 += s_sum[w][1];
+    }
   }
   if (tid >= 64) return;
   const double log_s = nan ? (double)__builtin_nanf("") : log(s0);
   auto prob = [&](float v) {
     if (v == m) return -log_s;
-    if (odd) return nan ? log_s : -(double)__builtin_inff();
+    if (endless) return nan ? log_s : -(double)__builtin_inff();
     return (double)P.scale * ((double)v - (double)m) - log_s;
   };
   if (tid == 0) {
@@ -217,52 +234,85 @@ __device__ __forceinline__ void finish_row(const LogprobParams& P, int t, const 
   }
 }
 
-// A workgroup: one piece of one row.
+// A wave's joined maximum, sums and rank, in every lane.
+__device__ __forceinline__ void join_wave(float& m, float& b, double& s0, double& s1) {
+  m = wave_max(m);
+  const float to = wave_max(b);
+  rebase(s0, s1, b, to);
+  b = to;
+  s0 = wave_sum64(s0);
+  s1 = wave_sum64(s1);
+}
+
+// A workgroup: one piece of one row.  A thread takes 8 logits at a time.
 template <bool F32, bool TOP>
 __global__ __launch_bounds__(kThreads) void k_logprob(LogprobParams P) {
-  constexpr int E = F32 ? 4 : 8;  // logits of a 16-byte load
-  __shared__ uint64_t s_buf[TOP ? kWaves : 1][128], s_list[TOP ? kWaves : 1][64];
-  __shared__ double s_s0[kWaves], s_s1[kWaves];
-  __shared__ float s_m[kWaves];
+  constexpr int E = 8, ES = F32 ? 4 : 2, NL = F32 ? 2 : 1;
+  __shared__ uint64_t s_buf[TOP ? kWaves : 1][128], s_list[TOP ? kWaves : 1][64], s_bar[kWaves];
+  __shared__ double s_sum[kWaves][2];
+  __shared__ float s_m[kWaves][2];
   __shared__ int s_rank[kWaves];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int t = (int)(blockIdx.x / P.splits), sp = (int)(blockIdx.x % P.splits);
-  const uint8_t* row = static_cast<const uint8_t*>(P.logits) + (int64_t)t * P.ld * (F32 ? 4 : 2);
+  const uint8_t* row = static_cast<const uint8_t*>(P.logits) + (int64_t)t * P.ld * ES;
   const int lo = sp * P.piece, hi = min(lo + P.piece, P.V);
-  const int id = P.ids ? P.ids[t] : -1;
-  const bool given = P.rank && id >= 0 && id < P.V;
-  const unsigned ahead = (unsigned)max(min(id, hi) - lo, 0);  // tokens of this piece with a lower id
+  const int id = P.rank ? P.ids[t] : -1;
+  const bool given = id >= 0 && id < P.V;
   const float gv = given ? logit<F32>(row, id) : __builtin_inff();  // nothing lies in front of +inf
-  // 16-byte pieces of the row's memory: piece q holds logits q * E - shift ..
-  const int shift = (int)(((uintptr_t)row & 15) / (F32 ? 4 : 2));
+  // the largest number below gv (for +-0: the least negative one): v > under says v >= gv (-inf has none: see below)
+  const uint32_t gu = __float_as_uint(gv);
+  const float under = (gu & 0x7FFFFFFFu) == 0u ? __uint_as_float(0x80000001u)
+                      : (gv == -__builtin_inff() ? gv : __uint_as_float((gu & 0x80000000u) ? gu + 1u : gu - 1u));
+  if constexpr (TOP) {
+    if (tid < kWaves) s_bar[tid] = 0;
+    __syncthreads();
+  }
+  // pieces of 8 logits of the row's memory, on 16-byte boundaries: piece q holds logits 8 q - shift ..
+  const int shift = (int)(((uintptr_t)row & 15) / ES);
   const int q0 = (lo + shift) / E, q1 = (hi + shift + E - 1) / E;
-  float m = -__builtin_inff(), s0 = 0.f, s1 = 0.f;
-  int rank = 0;
-  uint64_t list = 0, bar = 0;  // the wave's k best; the k-th
+  float m = -__builtin_inff(), b = kLeast, s0 = 0.f, s1 = 0.f;
+  int rank = 0;                 // uniform
+  uint64_t list = 0, bar = 0;   // the wave's k best; what a key has to pass (uniform)
   float bar_v = -__builtin_inff();
-  int held = 0;  // keys in the buffer (uniform)
+  int held = 0;                 // keys in the buffer (uniform)
+  auto raise = [&](uint64_t to) __attribute__((always_inline)) {
+    if (to > bar) {
+      bar = to;
+      bar_v = (uint32_t)(bar >> 32) == 0u ? -__builtin_inff() : key_value(bar);
+    }
+  };
   auto flush = [&](int n) {  // the buffer's first n <= 64 keys into the list
     const uint64_t key = lane < n ? s_buf[wave][lane] : 0u;
     list = merge64(list, sort64(key));
     const int l = P.k - 1;
-    bar = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(list >> 32), l) << 32) |
-          (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)list, l);
-    bar_v = key_value(bar);
+    const uint64_t kth = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(list >> 32), l) << 32) |
+                         (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)list, l);
+    if (lane == 0) s_bar[wave] = kth;
+    raise(kth);
   };
-  for (int qb = q0 + wave * 64; qb < q1; qb += kThreads) {
-    const int q = qb + lane, i0 = q * E - shift;
-    float v[E];
-    const bool whole = q < q1 && i0 >= lo && i0 + E <= hi;
-    if (whole) {
-      const uint4 u = *reinterpret_cast<const uint4*>(row + (int64_t)i0 * (F32 ? 4 : 2));
-      const uint32_t d[4] = {u.x, u.y, u.z, u.w};
+  auto whole = [&](int q) { return q < q1 && q * E - shift >= lo && q * E - shift + E <= hi; };
+  auto load = [&](int q, uint4 (&u)[NL]) __attribute__((always_inline)) {
+    if (whole(q)) {
+      const uint4* p = reinterpret_cast<const uint4*>(row + (int64_t)(q * E - shift) * ES);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (F32) {
-          v[j] = __uint_as_float(d[j]);
-        } else {
-          v[2 * j] = __uint_as_float(d[j] << 16);
-          v[2 * j + 1] = __uint_as_float(d[j] & 0xFFFF0000u);
+      for (int j = 0; j < NL; ++j) u[j] = p[j];
+    }
+  };
+  auto take = [&](int q, const uint4 (&u)[NL], bool first) __attribute__((always_inline)) {
+    const int i0 = q * E - shift;
+    float v[E];
+    if (whole(q)) {
+#pragma unroll
+      for (int j = 0; j < NL; ++j) {
+        const uint32_t d[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          if constexpr (F32) {
+            v[4 * j + w] = __uint_as_float(d[w]);
+          } else {
+            v[2 * w] = __uint_as_float(d[w] << 16);
+            v[2 * w + 1] = __uint_as_float(d[w] & 0xFFFF0000u);
+          }
         }
       }
     } else {  // the ends of the piece: what is not its own counts as -inf
@@ -276,26 +326,45 @@ __global__ __launch_bounds__(kThreads) void k_logprob(LogprobParams P) {
 #pragma unroll
     for (int j = 1; j < E; ++j) top = fmaxf(top, v[j]);
     if (top > m) {
-      rebase(s0, s1, m, top, P.c);
       m = top;
+      const float to = fmaxf(m * P.c, kLeast), d = fmaxf(b - to, -200.f), f = __builtin_amdgcn_exp2f(d);
+      s1 = f * fmaf(d, s0, s1);
+      s0 = f * s0;
+      b = to;
     }
-    const float base = m == -__builtin_inff() ? 0.f : m;
 #pragma unroll
     for (int j = 0; j < E; ++j) {
-      const float d = (v[j] - base) * P.c;
+      const float d = fmaf(v[j], P.c, -b);
       const float e = __builtin_amdgcn_exp2f(d);  // 0 at -inf; NaN stays
       s0 += e;
       s1 = fmaf(fmaxf(d, -200.f), e, s1);
     }
-    if (given && __any(top >= gv)) {
+    if (given) {
+      // equal logits count where their ids are lower; those of the given one's own 8 are looked at below
+      const float g = i0 + E <= id ? under : gv;
+      if (__any(top > g)) {
 #pragma unroll
-      for (int j = 0; j < E; ++j) rank += v[j] > gv || (v[j] == gv && (unsigned)(i0 + j - lo) < ahead);
+        for (int j = 0; j < E; ++j) rank += __popcll(__ballot(v[j] > g));
+      }
     }
     if constexpr (TOP) {
-      // equal logits of a higher id never pass a full list; one that is not full, or holds NaN, takes all
-      if ((uint32_t)(bar >> 32) == 0u || __any(top > bar_v)) {
+      if (first) {  // a bar from the lanes' largest: the k-th of them
+        uint32_t x = whole(q) ? (uint32_t)(key_of(top, 0) >> 32) : 0u;
+        x = (uint32_t)(sort64((uint64_t)x << 32) >> 32);
+        raise((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)x, P.k - 1) << 32);
+      }
+      if ((uint32_t)(bar >> 32) == 0u || __any(top >= bar_v)) {
+        // what the other waves hold counts too
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+          const uint64_t o = *(volatile uint64_t*)&s_bar[w];
+          raise(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(o >> 32)) << 32) |
+                (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)o));
+        }
 #pragma unroll
         for (int j = 0; j < E; ++j) {
+          // a list that is not full, or holds NaN, takes all
+          if ((uint32_t)(bar >> 32) != 0u && !__any(v[j] >= bar_v)) continue;
           const int i = i0 + j;
           const uint64_t key = q < q1 && i >= lo && i < hi ? key_of(v[j], i) : 0u;
           const bool pass = key > bar;
@@ -312,37 +381,57 @@ __global__ __launch_bounds__(kThreads) void k_logprob(LogprobParams P) {
         }
       }
     }
+  };
+  // two loads ahead
+  uint4 u0[NL], u1[NL];
+  int q = q0 + wave * 64;  // uniform
+  load(q + lane, u0);
+  load(q + kThreads + lane, u1);
+  for (bool first = true; q < q1; q += 2 * kThreads) {
+    take(q + lane, u0, first);
+    first = false;
+    load(q + 2 * kThreads + lane, u0);
+    if (q + kThreads < q1) {
+      take(q + kThreads + lane, u1, false);
+      load(q + 3 * kThreads + lane, u1);
+    }
   }
   if constexpr (TOP) {
     if (held > 0) flush(held);
     s_list[wave][lane] = list;
   }
+  if (given) {  // equal logits of the 8 that hold the given one; of -inf all
+    const bool least = gv == -__builtin_inff();
+    const int to = min(id, hi), from = least ? lo : max((id + shift) / E * E - shift, lo);
+    if (least || (id >= lo && id < hi))
+      for (int i = from + wave * 64; i < to; i += kThreads)  // uniform
+        rank += __popcll(__ballot(i + lane < to && logit<F32>(row, min(i + lane, to - 1)) == gv));
+  }
   // the waves' sums
-  const float wm = wave_max(m);
   double d0 = s0, d1 = s1;
-  rebase(d0, d1, m, wm, P.c);
-  d0 = wave_sum64(d0);
-  d1 = wave_sum64(d1);
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) rank += __shfl_xor(rank, d);
+  join_wave(m, b, d0, d1);
   if (lane == 0) {
-    s_m[wave] = wm;
-    s_s0[wave] = d0;
-    s_s1[wave] = d1;
+    s_m[wave][0] = m;
+    s_m[wave][1] = b;
+    s_sum[wave][0] = d0;
+    s_sum[wave][1] = d1;
     s_rank[wave] = rank;
   }
   __syncthreads();
-  float gm = s_m[0];
+  float gm = s_m[0][0], gb = s_m[0][1];
 #pragma unroll
-  for (int w = 1; w < kWaves; ++w) gm = fmaxf(gm, s_m[w]);
+  for (int w = 1; w < kWaves; ++w) {
+    gm = fmaxf(gm, s_m[w][0]);
+    gb = fmaxf(gb, s_m[w][1]);
+  }
   double g0 = 0, g1 = 0;
   int gr = 0;
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) {
-    double a = s_s0[w], b = s_s1[w];
-    rebase(a, b, s_m[w], gm, P.c);
-    g0 += a;
-    g1 += b;
+    double a0 = s_sum[w][0], a1 = s_sum[w][1];
+    rebase(a0, a1, s_m[w][1], gb);
+    g0 += a0;
+    g1 += a1;
     gr += s_rank[w];
   }
   if constexpr (TOP) {
@@ -352,70 +441,73 @@ __global__ __launch_bounds__(kThreads) void k_logprob(LogprobParams P) {
     }
   }
   if (P.splits == 1) {
-    finish_row<F32>(P, t, row, gm, g0, g1, gr, list);
+    finish_row<F32, kThreads>(P, t, row, gm, gb, g0, g1, gr, list);
     return;
   }
-  if (tid == 0) reinterpret_cast<Piece*>(P.ws)[blockIdx.x] = Piece{g0, g1, gm, gr};
+  if (tid == 0) reinterpret_cast<Piece*>(P.ws)[blockIdx.x] = Piece{g0, g1, gm, gb, gr, 0};
   if (TOP && tid < P.k)
     reinterpret_cast<uint64_t*>(P.ws + (int64_t)P.T * P.splits * sizeof(Piece))[(int64_t)blockIdx.x * P.k + tid] = list;
 }
 
-// A workgroup: one row from its pieces.
-template <bool F32, bool TOP>
-__global__ __launch_bounds__(kThreads) void k_logprob_join(LogprobParams P) {
-  __shared__ uint64_t s_list[TOP ? kWaves : 1][64];
+// A workgroup of NW waves: one row from its pieces, at most kMaxSplits.
+constexpr int kMaxSplits = 64;
+template <bool F32, bool TOP, int NW>
+__global__ __launch_bounds__(64 * NW) void k_logprob_join(LogprobParams P) {
+  __shared__ uint64_t s_list[TOP ? NW : 1][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, t = blockIdx.x;
   const uint8_t* row = static_cast<const uint8_t*>(P.logits) + (int64_t)t * P.ld * (F32 ? 4 : 2);
   const Piece* pc = reinterpret_cast<const Piece*>(P.ws) + (int64_t)t * P.splits;
+  // lane l: piece l
+  Piece p{0, 0, -__builtin_inff(), kLeast, 0, 0};
+  if (lane < P.splits) p = pc[lane];
   uint64_t list = 0;
   if constexpr (TOP) {
+    // the pieces' lists, those of a wave loaded at once
     const uint64_t* keys = reinterpret_cast<const uint64_t*>(P.ws + (int64_t)P.T * P.splits * sizeof(Piece)) +
                            (int64_t)t * P.splits * P.k;
-    for (int s = wave; s < P.splits; s += kWaves) {
-      const uint64_t b = lane < P.k ? keys[(int64_t)s * P.k + lane] : 0u;
-      list = merge64(list, b);
+    constexpr int PER = kMaxSplits / NW;
+    uint64_t k[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int s = wave + i * NW;
+      k[i] = s < P.splits && lane < P.k ? keys[(int64_t)s * P.k + lane] : 0u;
     }
+    list = k[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i)
+      if (i * NW < P.splits) list = merge64(list, k[i]);
     s_list[wave][lane] = list;
+    // pairs of waves, then pairs of those
+#pragma unroll
+    for (int h = NW / 2; h > 0; h /= 2) {
+      __syncthreads();
+      if (wave < h) {
+        list = merge64(list, s_list[wave + h][lane]);
+        s_list[wave][lane] = list;
+      }
+    }
   }
-  // every wave joins the sums: lane l those of pieces l, l + 64, ..
-  float m = -__builtin_inff();
-  for (int s = lane; s < P.splits; s += 64) m = fmaxf(m, pc[s].m);
-  m = wave_max(m);
-  double s0 = 0, s1 = 0;
-  int rank = 0;
-  for (int s = lane; s < P.splits; s += 64) {
-    double a = pc[s].s0, b = pc[s].s1;
-    rebase(a, b, pc[s].m, m, P.c);
-    s0 += a;
-    s1 += b;
-    rank += pc[s].rank;
-  }
-  s0 = wave_sum64(s0);
-  s1 = wave_sum64(s1);
+  float m = p.m, b = p.b;
+  double s0 = p.s0, s1 = p.s1;
+  join_wave(m, b, s0, s1);
+  int rank = p.rank;
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) rank += __shfl_xor(rank, d);
-  if constexpr (TOP) {
-    __syncthreads();
-    if (wave == 0) {
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) list = merge64(list, s_list[w][lane]);
-    }
-  }
-  finish_row<F32>(P, t, row, m, s0, s1, rank, list);
+  finish_row<F32, 64 * NW>(P, t, row, m, b, s0, s1, rank, list);
 }
 
 template <bool F32, bool TOP>
 void launch_logprob(const LogprobParams& P, hipStream_t s) {
   launch(k_logprob<F32, TOP>, dim3((unsigned)((int64_t)P.T * P.splits)), dim3(kThreads), 0, s, P);
-  if (P.splits > 1) launch(k_logprob_join<F32, TOP>, dim3((unsigned)P.T), dim3(kThreads), 0, s, P);
+  if (P.splits > 16 && TOP) launch(k_logprob_join<F32, TOP, 16>, dim3((unsigned)P.T), dim3(1024), 0, s, P);
+  else if (P.splits > 1) launch(k_logprob_join<F32, TOP, 4>, dim3((unsigned)P.T), dim3(256), 0, s, P);
 }
 
-// Pieces of a row: enough workgroups for the chip, none shorter than one
-// 16-byte load a thread.
-int row_splits(int T, int V, bool f32) {
-  const int least = kThreads * (f32 ? 4 : 8);
-  const int most = (V + least - 1) / least;
-  return std::max(1, std::min(most, 512 / T));
+// Pieces of a row: about eight workgroups a CU, none with less than 8 logits
+// a thread.
+int row_splits(int T, int V) {
+  const int most = (V + 8 * kThreads - 1) / (8 * kThreads);
+  return std::max(1, std::min({most, 2048 / T, kMaxSplits}));
 }
 
 bool bad_sizes(const moe_logprob_args* a) {
@@ -426,7 +518,7 @@ bool bad_sizes(const moe_logprob_args* a) {
 
 extern "C" size_t moe_logprobs_workspace_size(const moe_logprob_args* a) {
   if (!a || a->T < 1 || bad_sizes(a)) return 0;
-  const size_t n = row_splits(a->T, a->V, a->logits_f32 != 0);
+  const size_t n = row_splits(a->T, a->V);
   return n == 1 ? 0 : (size_t)a->T * n * (sizeof(Piece) + 8 * (size_t)a->k);
 }
 
@@ -454,7 +546,7 @@ extern "C" moe_status moe_logprobs(const moe_logprob_args* a, moe_stream_t strea
                        need);
     MOE_CHECK_ARG(((uintptr_t)a->workspace & 15) == 0, "moe_logprobs: workspace must lie on a 16-byte boundary");
   }
-  const int splits = row_splits(a->T, a->V, a->logits_f32 != 0);
+  const int splits = row_splits(a->T, a->V);
   // whole 16-byte loads a piece, as far as the row's start allows
   const int piece = ((a->V + splits - 1) / splits + 7) / 8 * 8;
   const LogprobParams P{a->T, a->V, a->logits, ld, a->scale, (float)((double)a->scale * 1.44269504088896340736), a->ids,
