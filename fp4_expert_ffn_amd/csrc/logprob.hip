@@ -12,11 +12,12 @@
 // Threads, waves and the pieces of a row are joined the same way, in 64 bits,
 // and b - c m is put back there: the largest logit counts as exactly 1.
 //
-// The k best are keys of 64 bits (the logit's order, then the lower id), which
-// a wave holds sorted over its lanes.  What passes the bar (the best k-th best
-// of the workgroup's waves; at first the k-th best of the lanes' largest) is
-// gathered in LDS, and every 64 of them are sorted and merged into the list:
-// no order of the logits costs more than one sort per 64.
+// The k best are keys of 64 bits (the logit's order, then the lower id).  A
+// wave gathers in LDS what passes the bar: at first the k-th best of its lanes'
+// largest, later the best k-th best of the workgroup's waves.  When 3 k have
+// gathered, the upper 16 bits of the k-th are found bit by bit with ballots,
+// become the bar, and what lies below goes: whatever the order of the logits, a
+// key is looked at a few times.  Only the row's last 64 are sorted.
 //
 // Ranks are counted by ballots, on the scalar unit, and only where some lane's
 // largest reaches the given logit.
@@ -24,6 +25,7 @@
 // Rows whose c m is beyond 1e8, infinite ones among them, or that hold a NaN,
 // are summed once more, in 64 bits (finish_row).
 #include <algorithm>
+#include <cstdlib>
 
 #include "common.h"
 #include "wave.h"
@@ -49,7 +51,7 @@ struct LogprobParams {
   int32_t* top_ids;
   float* top_logprob;
   int splits, piece;  // logits a piece
-  uint8_t* ws;        // splits > 1: [T * splits] Piece, then [T * splits][k] keys
+  uint8_t* ws;        // splits > 1: [T * splits] Piece, then with k [T * splits][64] keys
 };
 
 // What a piece of a row leaves: its maximum, the two sums against b, and the
@@ -57,7 +59,7 @@ struct LogprobParams {
 struct Piece {
   double s0, s1;
   float m, b;
-  int rank, pad;
+  int rank, held;  // held: keys it leaves, 64 at most
 };
 
 // The order of tokens as one number: the logit's order (equal values equal,
@@ -120,22 +122,136 @@ __device__ __forceinline__ uint64_t settle(uint64_t v) {
   return v;
 }
 
-// 64 keys in descending order over the lanes: runs of twice the length by a
-// first step against the mirrored partner.
-__device__ __forceinline__ uint64_t sort64(uint64_t v) {
+// Keys in descending order over the lanes, all but the first n (uniform) of
+// them 0: runs of twice the length by a first step against the mirrored
+// partner, as far as there are keys.
+__device__ __forceinline__ uint64_t sort64(uint64_t v, int n) {
   v = exchange<1, 1>(v);
   v = settle<1>(exchange<3, 2>(v));
-  v = settle<2>(exchange<7, 4>(v));
-  v = settle<4>(exchange<15, 8>(v));
-  v = settle<8>(exchange<31, 16>(v));
-  return settle<16>(exchange<63, 32>(v));
+  if (n > 4) v = settle<2>(exchange<7, 4>(v));
+  if (n > 8) v = settle<4>(exchange<15, 8>(v));
+  if (n > 16) v = settle<8>(exchange<31, 16>(v));
+  if (n > 32) v = settle<16>(exchange<63, 32>(v));
+  return v;
 }
 
-// The 64 best of two descending lists, descending.
-__device__ __forceinline__ uint64_t merge64(uint64_t a, uint64_t b) {
-  const uint64_t r = lane_xor64<63>(b);
-  return settle<32>(a > r ? a : r);
+// The k-th largest of the lanes' 32-bit keys, n registers of them, its lower
+// half cut off (0: there are fewer; uniform).
+template <int N>
+__device__ __forceinline__ uint32_t kth_of_lanes(const uint32_t (&x)[N], int n, int k) {
+  uint32_t t = 0;
+#pragma unroll 1
+  for (uint32_t bit = 1u << 31; bit >= 1u << 16; bit >>= 1) {
+    const uint32_t c = t | bit;
+    int have = __popcll(__ballot(x[0] >= c));
+#pragma unroll
+    for (int i = 1; i < N; ++i)
+      if (i < n) have += __popcll(__ballot(x[i] >= c));
+    t = have >= k ? c : t;
+  }
+  return t;
 }
+
+// The workgroup's bar, in LDS: the largest of its waves'.
+__device__ __forceinline__ uint64_t shared_bar(uint64_t* s_bar) {
+  const uint64_t o = __hip_atomic_load(s_bar, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+  return ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(o >> 32)) << 32) |
+         (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)o);
+}
+__device__ __forceinline__ void raise_shared(uint64_t* s_bar, uint64_t to) {
+  if ((threadIdx.x & 63) == 0) __hip_atomic_fetch_max(s_bar, to, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+}
+
+// A wave's keys, unordered, in LDS.
+constexpr int kKeys = 256;
+struct Keys {
+  uint64_t* at;  // [kKeys]
+  int k, held;   // how many are wanted; uniform
+  int limit;     // held beyond it: time to cut
+  uint64_t bar;  // what a key has to pass (uniform); 0: all do
+  float bar_v;   // its logit; -inf where it is no number's
+
+  // Until it is cut the bar stands, and the share of logits that pass it, and
+  // go the long way, is k to what had been seen when it was set; a cut costs as
+  // much as some ten additions.
+  __device__ __forceinline__ Keys(uint64_t* lds, int wanted, int least)
+      : at(lds), k(wanted), held(0), limit(min(kKeys - 64, max(least, 3 * k))), bar(0), bar_v(-__builtin_inff()) {}
+  __device__ __forceinline__ void raise(uint64_t to) {
+    if (to > bar) {
+      bar = to;
+      bar_v = (uint32_t)(bar >> 32) < 0x007FFFFFu ? -__builtin_inff() : key_value(bar);  // below the key of -inf
+    }
+  }
+  // Takes the lanes' keys that pass; 64 places at least are free.
+  __device__ __forceinline__ void add(uint64_t key) {
+    const bool pass = key > bar;
+    const uint64_t mask = __ballot(pass);
+    if (pass) at[held + __popcll(mask & ((1ull << (threadIdx.x & 63)) - 1))] = key;
+    held += __popcll(mask);
+    __builtin_amdgcn_wave_barrier();  // a wave's LDS accesses keep their order
+  }
+  // Keeps the k best and those that share the upper 16 bits with the k-th, 64 at
+  // most in all; raises the bar to those bits.
+  __device__ __forceinline__ void cut() {
+    const int lane = threadIdx.x & 63;
+    constexpr int N = kKeys / 64;
+    const int n = (held + 63) / 64;
+    uint64_t r[N];
+    uint32_t x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      r[i] = i * 64 + lane < held ? at[i * 64 + lane] : 0u;
+      x[i] = (uint32_t)(r[i] >> 32);
+    }
+    uint64_t t = (uint64_t)kth_of_lanes(x, n, k) << 32;
+    int have = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) have += __popcll(__ballot(r[i] != 0u && r[i] >= t));
+    if (have > 64) {  // many equal logits: the k-th key itself
+      for (uint64_t bit = 1ull << 47; bit; bit >>= 1) {
+        const uint64_t c = t | bit;
+        have = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) have += __popcll(__ballot(r[i] >= c));
+        if (have >= k) t = c;
+        if (have == k) break;
+      }
+    }
+    const uint64_t low = t ? t - 1 : 0u;  // keys are whole numbers: what reaches t passes
+    held = 0;
+    bar = low;
+#pragma unroll
+    for (int i = 0; i < N; ++i) add(r[i]);
+    bar = 0;
+    raise(low);
+    limit = min(kKeys - 64, max(limit, 2 * held));
+  }
+  // Cuts where the limit is passed; the workgroup's bar follows.
+  __device__ __forceinline__ void room(uint64_t* s_bar) {
+    if (held > limit) {
+      const uint64_t had = bar;
+      cut();
+      raise_shared(s_bar, bar);
+      raise(had);
+    }
+  }
+  // A wave's keys, 64 at most, and its bar for wave 0 ..
+  __device__ __forceinline__ void publish(int* s_held, uint64_t* s_bar, int wave) {
+    if (held > 64) cut();
+    if ((threadIdx.x & 63) == 0) s_held[wave] = held;
+    raise_shared(s_bar, bar);
+  }
+  // .. which adds the others' to its own, behind a barrier: one a lane, unordered.
+  // The waves' keys lie kKeys apart.
+  __device__ __forceinline__ uint64_t gather(const int* s_held, uint64_t* s_bar) {
+    const int lane = threadIdx.x & 63;
+    raise(shared_bar(s_bar));
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) add(lane < s_held[w] ? at[w * kKeys + lane] : 0u);
+    if (held > 64) cut();
+    return lane < held ? at[lane] : 0u;
+  }
+};
 
 __device__ __forceinline__ double wave_sum64(double v) {
 #pragma unroll
@@ -151,16 +267,29 @@ __device__ __forceinline__ float wave_max(float v) {
   return max_rows4(v);
 }
 
-// Sums taken against b as sums against `to`.
-__device__ __forceinline__ void rebase(double& s0, double& s1, double b, double to) {
-  const double d = fmax(b - to, -1000.0), f = exp2(d);
-  s1 = f * (s1 + d * s0);
+// Sums taken against b as sums against `to`.  The factor in fp32: a part of
+// the sum is off by 2^-23 of itself.
+__device__ __forceinline__ void rebase(double& s0, double& s1, float b, float to) {
+  const float d = fmaxf(b - to, -1000.f);
+  const double f = (double)__builtin_amdgcn_exp2f(d);
+  s1 = f * (s1 + (double)d * s0);
   s0 = f * s0;
 }
 
 template <bool F32>
 __device__ __forceinline__ float logit(const void* row, int i) {
   return F32 ? static_cast<const float*>(row)[i] : bf16_to_f32(static_cast<const uint16_t*>(row)[i]);
+}
+
+// A row's given token; its logit, NaN where there is none.
+struct Given {
+  int id;
+  float v;
+};
+template <bool F32>
+__device__ __forceinline__ Given given_of(const LogprobParams& P, int t, const void* row) {
+  const int id = P.ids ? P.ids[t] : -1;
+  return Given{id, id >= 0 && id < P.V ? logit<F32>(row, id) : __builtin_nanf("")};
 }
 
 // b, rounded, is off by up to 2^-24 |c m|: 2^(c m - b), which the joins put
@@ -170,8 +299,8 @@ constexpr float kHuge = 1e8f, kLeast = -1e8f;
 // The outputs of a row from its joined sums against b, by the whole workgroup
 // of NT threads: lane l of wave 0 holds the l-th best key.
 template <bool F32, int NT>
-__device__ __forceinline__ void finish_row(const LogprobParams& P, int t, const void* row, float m, float b, double s0,
-                                           double s1, int rank, uint64_t best) {
+__device__ __forceinline__ void finish_row(const LogprobParams& P, int t, const void* row, Given gt, float m, float b,
+                                           double s0, double s1, int rank, uint64_t best) {
   __shared__ double s_sum[NT / 64][2];
   __shared__ int s_nan;
   const int tid = threadIdx.x;
@@ -180,7 +309,9 @@ __device__ __forceinline__ void finish_row(const LogprobParams& P, int t, const 
   const bool odd = !(fabs(mc) < (double)kHuge) || s0 != s0;
   bool nan = false;
   if (!odd) {
-    rebase(s0, s1, b, mc);
+    const double d = (double)b - mc, f = exp2(d);
+    s1 = f * (s1 + d * s0);
+    s0 = f * s0;
   } else {  // uniform: the sums once more.  An endless m: tokens equal to it share the row
     if (tid == 0) s_nan = 0;
     __syncthreads();
@@ -219,13 +350,8 @@ __device__ __forceinline__ void finish_row(const LogprobParams& P, int t, const 
   if (tid == 0) {
     if (P.lse) P.lse[t] = (float)((double)P.scale * (double)m + log_s);
     if (P.entropy) P.entropy[t] = (float)(log_s - s1 * 0.69314718055994530942 / s0);
-    if (P.ids) {
-      const int id = P.ids[t];
-      const bool in = id >= 0 && id < P.V;
-      const float v = in ? logit<F32>(row, id) : __builtin_nanf("");
-      if (P.logprob) P.logprob[t] = id < 0 ? 0.f : (v != v ? __builtin_nanf("") : (float)prob(v));
-      if (P.rank) P.rank[t] = v != v ? -1 : rank;
-    }
+    if (P.logprob) P.logprob[t] = gt.id < 0 ? 0.f : (gt.v != gt.v ? __builtin_nanf("") : (float)prob(gt.v));
+    if (P.rank) P.rank[t] = gt.v != gt.v ? -1 : rank;
   }
   if (tid < P.k) {
     const float v = key_value(best);
@@ -248,7 +374,8 @@ __device__ __forceinline__ void join_wave(float& m, float& b, double& s0, double
 template <bool F32, bool TOP>
 __global__ __launch_bounds__(kThreads) void k_logprob(LogprobParams P) {
   constexpr int E = 8, ES = F32 ? 4 : 2, NL = F32 ? 2 : 1;
-  __shared__ uint64_t s_buf[TOP ? kWaves : 1][128], s_list[TOP ? kWaves : 1][64], s_bar[kWaves];
+  __shared__ uint64_t s_keys[TOP ? kWaves : 1][kKeys], s_bar;
+  __shared__ int s_held[kWaves];
   __shared__ double s_sum[kWaves][2];
   __shared__ float s_m[kWaves][2];
   __shared__ int s_rank[kWaves];
@@ -256,15 +383,16 @@ __global__ __launch_bounds__(kThreads) void k_logprob(LogprobParams P) {
   const int t = (int)(blockIdx.x / P.splits), sp = (int)(blockIdx.x % P.splits);
   const uint8_t* row = static_cast<const uint8_t*>(P.logits) + (int64_t)t * P.ld * ES;
   const int lo = sp * P.piece, hi = min(lo + P.piece, P.V);
-  const int id = P.rank ? P.ids[t] : -1;
-  const bool given = id >= 0 && id < P.V;
-  const float gv = given ? logit<F32>(row, id) : __builtin_inff();  // nothing lies in front of +inf
+  const Given gt = given_of<F32>(P, t, row);
+  const int id = gt.id;
+  const bool given = P.rank && id >= 0 && id < P.V;
+  const float gv = given ? gt.v : __builtin_inff();  // nothing lies in front of +inf
   // the largest number below gv (for +-0: the least negative one): v > under says v >= gv (-inf has none: see below)
   const uint32_t gu = __float_as_uint(gv);
   const float under = (gu & 0x7FFFFFFFu) == 0u ? __uint_as_float(0x80000001u)
                       : (gv == -__builtin_inff() ? gv : __uint_as_float((gu & 0x80000000u) ? gu + 1u : gu - 1u));
   if constexpr (TOP) {
-    if (tid < kWaves) s_bar[tid] = 0;
+    if (tid == 0) s_bar = 0;
     __syncthreads();
   }
   // pieces of 8 logits of the row's memory, on 16-byte boundaries: piece q holds logits 8 q - shift ..
@@ -272,24 +400,7 @@ __global__ __launch_bounds__(kThreads) void k_logprob(LogprobParams P) {
   const int q0 = (lo + shift) / E, q1 = (hi + shift + E - 1) / E;
   float m = -__builtin_inff(), b = kLeast, s0 = 0.f, s1 = 0.f;
   int rank = 0;                 // uniform
-  uint64_t list = 0, bar = 0;   // the wave's k best; what a key has to pass (uniform)
-  float bar_v = -__builtin_inff();
-  int held = 0;                 // keys in the buffer (uniform)
-  auto raise = [&](uint64_t to) __attribute__((always_inline)) {
-    if (to > bar) {
-      bar = to;
-      bar_v = (uint32_t)(bar >> 32) == 0u ? -__builtin_inff() : key_value(bar);
-    }
-  };
-  auto flush = [&](int n) {  // the buffer's first n <= 64 keys into the list
-    const uint64_t key = lane < n ? s_buf[wave][lane] : 0u;
-    list = merge64(list, sort64(key));
-    const int l = P.k - 1;
-    const uint64_t kth = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(list >> 32), l) << 32) |
-                         (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)list, l);
-    if (lane == 0) s_bar[wave] = kth;
-    raise(kth);
-  };
+  Keys keys(s_keys[TOP ? wave : 0], P.k, P.piece <= 16 * E * kThreads ? 64 : 8);
   auto whole = [&](int q) { return q < q1 && q * E - shift >= lo && q * E - shift + E <= hi; };
   auto load = [&](int q, uint4 (&u)[NL]) __attribute__((always_inline)) {
     if (whole(q)) {
@@ -298,9 +409,7 @@ __global__ __launch_bounds__(kThreads) void k_logprob(LogprobParams P) {
       for (int j = 0; j < NL; ++j) u[j] = p[j];
     }
   };
-  auto take = [&](int q, const uint4 (&u)[NL], bool first) __attribute__((always_inline)) {
-    const int i0 = q * E - shift;
-    float v[E];
+  auto unpack = [&](int q, const uint4 (&u)[NL], float (&v)[E]) __attribute__((always_inline)) {
     if (whole(q)) {
 #pragma unroll
       for (int j = 0; j < NL; ++j) {
@@ -318,10 +427,13 @@ __global__ __launch_bounds__(kThreads) void k_logprob(LogprobParams P) {
     } else {  // the ends of the piece: what is not its own counts as -inf
 #pragma unroll
       for (int j = 0; j < E; ++j) {
-        const int i = i0 + j;
+        const int i = q * E - shift + j;
         v[j] = q < q1 && i >= lo && i < hi ? logit<F32>(row, i) : -__builtin_inff();
       }
     }
+  };
+  auto take = [&](int q, const float (&v)[E], bool first) __attribute__((always_inline)) {
+    const int i0 = q * E - shift;
     float top = v[0];
 #pragma unroll
     for (int j = 1; j < E; ++j) top = fmaxf(top, v[j]);
@@ -349,57 +461,50 @@ __global__ __launch_bounds__(kThreads) void k_logprob(LogprobParams P) {
     }
     if constexpr (TOP) {
       if (first) {  // a bar from the lanes' largest: the k-th of them
-        uint32_t x = whole(q) ? (uint32_t)(key_of(top, 0) >> 32) : 0u;
-        x = (uint32_t)(sort64((uint64_t)x << 32) >> 32);
-        raise((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)x, P.k - 1) << 32);
+        const uint32_t x[1] = {whole(q) ? (uint32_t)(key_of(top, 0) >> 32) : 0u};
+        keys.raise((uint64_t)kth_of_lanes(x, 1, P.k) << 32);
       }
-      if ((uint32_t)(bar >> 32) == 0u || __any(top >= bar_v)) {
-        // what the other waves hold counts too
+      // a bar below all numbers lets NaN pass too
+      if ((uint32_t)(keys.bar >> 32) == 0u || __any(top >= keys.bar_v)) {
+        keys.raise(shared_bar(&s_bar));  // what the other waves hold counts too
+        const bool own = q < q1;
+        // each lane's first largest, one for all lanes; then what more there is
+        int at = 0, n = 0;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-          const uint64_t o = *(volatile uint64_t*)&s_bar[w];
-          raise(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(o >> 32)) << 32) |
-                (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)o));
+        for (int j = E - 1; j >= 0; --j) {
+          at = v[j] == top ? j : at;
+          n += v[j] >= keys.bar_v;
         }
+        const bool all = (uint32_t)(keys.bar >> 32) == 0u;  // NaN passes too: one by one
+        if (!all) keys.add(own && i0 + at >= lo && i0 + at < hi ? key_of(top, i0 + at) : 0u);
+        if (all || __any(n > 1)) {
+#pragma unroll 1
+          for (int j = 0; j < E; ++j) {
+            float x = v[0];
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-          // a list that is not full, or holds NaN, takes all
-          if ((uint32_t)(bar >> 32) != 0u && !__any(v[j] >= bar_v)) continue;
-          const int i = i0 + j;
-          const uint64_t key = q < q1 && i >= lo && i < hi ? key_of(v[j], i) : 0u;
-          const bool pass = key > bar;
-          const uint64_t mask = __ballot(pass);
-          if (pass) s_buf[wave][held + __popcll(mask & ((1ull << lane) - 1))] = key;
-          held += __popcll(mask);
-          __builtin_amdgcn_wave_barrier();  // a wave's LDS accesses keep their order
-          if (held >= 64) {
-            flush(64);
-            if (lane < held - 64) s_buf[wave][lane] = s_buf[wave][64 + lane];
-            __builtin_amdgcn_wave_barrier();
-            held -= 64;
+            for (int o = 1; o < E; ++o) x = j == o ? v[o] : x;
+            const int i = i0 + j;
+            keys.room(&s_bar);
+            if (all || __any(x >= keys.bar_v && j != at))
+              keys.add(own && i >= lo && i < hi && (all || j != at) ? key_of(x, i) : 0u);
           }
         }
+        keys.room(&s_bar);
       }
     }
   };
-  // two loads ahead
-  uint4 u0[NL], u1[NL];
+  // a load ahead: with eight waves a SIMD it has their whole turn to land
+  uint4 u[NL];
   int q = q0 + wave * 64;  // uniform
-  load(q + lane, u0);
-  load(q + kThreads + lane, u1);
-  for (bool first = true; q < q1; q += 2 * kThreads) {
-    take(q + lane, u0, first);
-    first = false;
-    load(q + 2 * kThreads + lane, u0);
-    if (q + kThreads < q1) {
-      take(q + kThreads + lane, u1, false);
-      load(q + 3 * kThreads + lane, u1);
-    }
+  load(q + lane, u);
+#pragma unroll 1
+  for (bool first = true; q < q1; q += kThreads, first = false) {
+    float v[E];
+    unpack(q + lane, u, v);
+    load(q + kThreads + lane, u);
+    take(q + lane, v, first);
   }
-  if constexpr (TOP) {
-    if (held > 0) flush(held);
-    s_list[wave][lane] = list;
-  }
+  if constexpr (TOP) keys.publish(s_held, &s_bar, wave);
   if (given) {  // equal logits of the 8 that hold the given one; of -inf all
     const bool least = gv == -__builtin_inff();
     const int to = min(id, hi), from = least ? lo : max((id + shift) / E * E - shift, lo);
@@ -434,57 +539,68 @@ __global__ __launch_bounds__(kThreads) void k_logprob(LogprobParams P) {
     g1 += a1;
     gr += s_rank[w];
   }
+  uint64_t best = 0;  // wave 0: the piece's best, 64 at most, one a lane, unordered
   if constexpr (TOP) {
-    if (wave == 0) {
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) list = merge64(list, s_list[w][lane]);
-    }
+    if (wave == 0) best = keys.gather(s_held, &s_bar);
   }
   if (P.splits == 1) {
-    finish_row<F32, kThreads>(P, t, row, gm, gb, g0, g1, gr, list);
+    if (TOP && wave == 0) best = sort64(best, keys.held);
+    finish_row<F32, kThreads>(P, t, row, gt, gm, gb, g0, g1, gr, best);
     return;
   }
-  if (tid == 0) reinterpret_cast<Piece*>(P.ws)[blockIdx.x] = Piece{g0, g1, gm, gb, gr, 0};
-  if (TOP && tid < P.k)
-    reinterpret_cast<uint64_t*>(P.ws + (int64_t)P.T * P.splits * sizeof(Piece))[(int64_t)blockIdx.x * P.k + tid] = list;
+  if (tid == 0) reinterpret_cast<Piece*>(P.ws)[blockIdx.x] = Piece{g0, g1, gm, gb, gr, keys.held};
+  if (TOP && tid < keys.held)  // wave 0's
+    reinterpret_cast<uint64_t*>(P.ws + (int64_t)P.T * P.splits * sizeof(Piece))[(int64_t)blockIdx.x * 64 + tid] = best;
 }
 
-// A workgroup of NW waves: one row from its pieces, at most kMaxSplits.
+// A workgroup: one row from its pieces, at most kMaxSplits.  Every wave joins
+// the sums (lane l: piece l) and takes every fourth piece's best.
 constexpr int kMaxSplits = 64;
-template <bool F32, bool TOP, int NW>
-__global__ __launch_bounds__(64 * NW) void k_logprob_join(LogprobParams P) {
-  __shared__ uint64_t s_list[TOP ? NW : 1][64];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, t = blockIdx.x;
+template <bool F32, bool TOP>
+__global__ __launch_bounds__(kThreads) void k_logprob_join(LogprobParams P) {
+  __shared__ uint64_t s_keys[TOP ? kWaves : 1][kKeys], s_bar;
+  __shared__ int s_held[kWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), t = blockIdx.x;
   const uint8_t* row = static_cast<const uint8_t*>(P.logits) + (int64_t)t * P.ld * (F32 ? 4 : 2);
   const Piece* pc = reinterpret_cast<const Piece*>(P.ws) + (int64_t)t * P.splits;
-  // lane l: piece l
+  const Given gt = given_of<F32>(P, t, row);
   Piece p{0, 0, -__builtin_inff(), kLeast, 0, 0};
   if (lane < P.splits) p = pc[lane];
-  uint64_t list = 0;
+  uint64_t best = 0;
   if constexpr (TOP) {
-    // the pieces' lists, those of a wave loaded at once
-    const uint64_t* keys = reinterpret_cast<const uint64_t*>(P.ws + (int64_t)P.T * P.splits * sizeof(Piece)) +
-                           (int64_t)t * P.splits * P.k;
-    constexpr int PER = kMaxSplits / NW;
-    uint64_t k[PER];
+    const uint64_t* src = reinterpret_cast<const uint64_t*>(P.ws + (int64_t)P.T * P.splits * sizeof(Piece)) +
+                          (int64_t)t * P.splits * 64 + lane;
+    if (tid == 0) s_bar = 0;
+    __syncthreads();
+    Keys keys(s_keys[wave], P.k, 64);
+    // the k-th best of the pieces' largest is a bar (-inf may stand for a piece of nothing but NaN)
+    const uint32_t x[1] = {p.m > -__builtin_inff() ? (uint32_t)(key_of(p.m, 0) >> 32) : 0u};
+    const uint32_t least = kth_of_lanes(x, 1, P.k);
+    keys.raise((uint64_t)least << 32);
+    uint64_t todo = __ballot(p.held > 0 && x[0] >= least) & (0x1111111111111111ull << wave);  // pieces that can pass it
+    constexpr int U = 8;                                                                      // loaded at once
+    while (todo) {
+      uint64_t v[U];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int s = wave + i * NW;
-      k[i] = s < P.splits && lane < P.k ? keys[(int64_t)s * P.k + lane] : 0u;
-    }
-    list = k[0];
-#pragma unroll
-    for (int i = 1; i < PER; ++i)
-      if (i * NW < P.splits) list = merge64(list, k[i]);
-    s_list[wave][lane] = list;
-    // pairs of waves, then pairs of those
-#pragma unroll
-    for (int h = NW / 2; h > 0; h /= 2) {
-      __syncthreads();
-      if (wave < h) {
-        list = merge64(list, s_list[wave + h][lane]);
-        s_list[wave][lane] = list;
+      for (int u = 0; u < U; ++u) {
+        const int s = todo ? __builtin_ctzll(todo) : 0;
+        v[u] = todo && lane < __builtin_amdgcn_readlane(p.held, s) ? src[s * 64] : 0u;
+        todo &= todo - 1;  // 0 stays 0
       }
+#pragma unroll 1
+      for (int u = 0; u < U; ++u) {
+        uint64_t y = v[0];
+#pragma unroll
+        for (int o = 1; o < U; ++o) y = u == o ? v[o] : y;
+        keys.add(y);
+        if (keys.held > kKeys - 64) keys.cut();
+      }
+    }
+    keys.publish(s_held, &s_bar, wave);
+    __syncthreads();
+    if (wave == 0) {
+      best = keys.gather(s_held, &s_bar);
+      best = sort64(best, keys.held);
     }
   }
   float m = p.m, b = p.b;
@@ -493,21 +609,22 @@ __global__ __launch_bounds__(64 * NW) void k_logprob_join(LogprobParams P) {
   int rank = p.rank;
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) rank += __shfl_xor(rank, d);
-  finish_row<F32, 64 * NW>(P, t, row, m, b, s0, s1, rank, list);
+  finish_row<F32, kThreads>(P, t, row, gt, m, b, s0, s1, rank, best);
 }
 
 template <bool F32, bool TOP>
 void launch_logprob(const LogprobParams& P, hipStream_t s) {
   launch(k_logprob<F32, TOP>, dim3((unsigned)((int64_t)P.T * P.splits)), dim3(kThreads), 0, s, P);
-  if (P.splits > 16 && TOP) launch(k_logprob_join<F32, TOP, 16>, dim3((unsigned)P.T), dim3(1024), 0, s, P);
-  else if (P.splits > 1) launch(k_logprob_join<F32, TOP, 4>, dim3((unsigned)P.T), dim3(256), 0, s, P);
+  if (P.splits > 1) launch(k_logprob_join<F32, TOP>, dim3((unsigned)P.T), dim3(kThreads), 0, s, P);
 }
 
-// Pieces of a row: about eight workgroups a CU, none with less than 8 logits
-// a thread.
-int row_splits(int T, int V) {
+// Pieces of a row: about eight workgroups a CU, four where each makes a list
+// of its own; none with less than 8 logits a thread.
+int row_splits(int T, int V, int k) {
   const int most = (V + 8 * kThreads - 1) / (8 * kThreads);
-  return std::max(1, std::min({most, 2048 / T, kMaxSplits}));
+  int wg = k ? 1024 : 2048;
+  if (const char* e = getenv("LP_WG")) wg = atoi(e);
+  return std::max(1, std::min({most, wg / T, kMaxSplits}));
 }
 
 bool bad_sizes(const moe_logprob_args* a) {
@@ -518,8 +635,8 @@ bool bad_sizes(const moe_logprob_args* a) {
 
 extern "C" size_t moe_logprobs_workspace_size(const moe_logprob_args* a) {
   if (!a || a->T < 1 || bad_sizes(a)) return 0;
-  const size_t n = row_splits(a->T, a->V);
-  return n == 1 ? 0 : (size_t)a->T * n * (sizeof(Piece) + 8 * (size_t)a->k);
+  const size_t n = row_splits(a->T, a->V, a->k);
+  return n == 1 ? 0 : (size_t)a->T * n * (sizeof(Piece) + (a->k ? 64 * 8 : 0));
 }
 
 extern "C" moe_status moe_logprobs(const moe_logprob_args* a, moe_stream_t stream) {
@@ -546,7 +663,7 @@ extern "C" moe_status moe_logprobs(const moe_logprob_args* a, moe_stream_t strea
                        need);
     MOE_CHECK_ARG(((uintptr_t)a->workspace & 15) == 0, "moe_logprobs: workspace must lie on a 16-byte boundary");
   }
-  const int splits = row_splits(a->T, a->V);
+  const int splits = row_splits(a->T, a->V, a->k);
   // whole 16-byte loads a piece, as far as the row's start allows
   const int piece = ((a->V + splits - 1) / splits + 7) / 8 * 8;
   const LogprobParams P{a->T, a->V, a->logits, ld, a->scale, (float)((double)a->scale * 1.44269504088896340736), a->ids,
