@@ -467,29 +467,22 @@ __global__ __launch_bounds__(kThreads) void k_logprob(LogprobParams P) {
       // a bar below all numbers lets NaN pass too
       if ((uint32_t)(keys.bar >> 32) == 0u || __any(top >= keys.bar_v)) {
         keys.raise(shared_bar(&s_bar));  // what the other waves hold counts too
-        const bool own = q < q1;
-        // each lane's first largest, one for all lanes; then what more there is
-        int at = 0, n = 0;
+        // the lane's logits that reach it, each of its own lane's in turn: mostly one turn
+        const bool all = (uint32_t)(keys.bar >> 32) == 0u;  // NaN passes too
+        uint32_t left = 0;
 #pragma unroll
-        for (int j = E - 1; j >= 0; --j) {
-          at = v[j] == top ? j : at;
-          n += v[j] >= keys.bar_v;
-        }
-        const bool all = (uint32_t)(keys.bar >> 32) == 0u;  // NaN passes too: one by one
-        if (!all) keys.add(own && i0 + at >= lo && i0 + at < hi ? key_of(top, i0 + at) : 0u);
-        if (all || __any(n > 1)) {
+        for (int j = 0; j < E; ++j)
+          left |= (all || v[j] >= keys.bar_v) && q < q1 && i0 + j >= lo && i0 + j < hi ? 1u << j : 0u;
 #pragma unroll 1
-          for (int j = 0; j < E; ++j) {
-            float x = v[0];
+        while (__any(left != 0u)) {
+          const int j = left ? __builtin_ctz(left) : 0;
+          float x = v[0];
 #pragma unroll
-            for (int o = 1; o < E; ++o) x = j == o ? v[o] : x;
-            const int i = i0 + j;
-            keys.room(&s_bar);
-            if (all || __any(x >= keys.bar_v && j != at))
-              keys.add(own && i >= lo && i < hi && (all || j != at) ? key_of(x, i) : 0u);
-          }
+          for (int o = 1; o < E; ++o) x = j == o ? v[o] : x;
+          keys.add(left ? key_of(x, i0 + j) : 0u);
+          left &= left - 1u;  // 0 stays 0
+          keys.room(&s_bar);
         }
-        keys.room(&s_bar);
       }
     }
   };
