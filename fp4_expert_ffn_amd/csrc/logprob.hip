@@ -25,7 +25,6 @@
 // Rows whose c m is beyond 1e8, infinite ones among them, or that hold a NaN,
 // are summed once more, in 64 bits (finish_row).
 #include <algorithm>
-#include <cstdlib>
 
 #include "common.h"
 #include "wave.h"
@@ -573,6 +572,7 @@ __global__ __launch_bounds__(kThreads) void k_logprob_join(LogprobParams P) {
     uint64_t todo = __ballot(p.held > 0 && x[0] >= least) & (0x1111111111111111ull << wave);  // pieces that can pass it
     constexpr int U = 8;                                                                      // loaded at once
     while (todo) {
+      const int n = min(__popcll(todo), U);
       uint64_t v[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -581,7 +581,7 @@ __global__ __launch_bounds__(kThreads) void k_logprob_join(LogprobParams P) {
         todo &= todo - 1;  // 0 stays 0
       }
 #pragma unroll 1
-      for (int u = 0; u < U; ++u) {
+      for (int u = 0; u < n; ++u) {
         uint64_t y = v[0];
 #pragma unroll
         for (int o = 1; o < U; ++o) y = u == o ? v[o] : y;
@@ -611,13 +611,12 @@ void launch_logprob(const LogprobParams& P, hipStream_t s) {
   if (P.splits > 1) launch(k_logprob_join<F32, TOP>, dim3((unsigned)P.T), dim3(kThreads), 0, s, P);
 }
 
-// Pieces of a row: about eight workgroups a CU, four where each makes a list
-// of its own; none with less than 8 logits a thread.
-int row_splits(int T, int V, int k) {
+// Pieces of a row: about four workgroups a CU, none with less than 8 logits a
+// thread.  us with 512, 1024 and 2048 workgroups: 333 rows of 50021 fp32 logits,
+// k = 5, 36, 33 and 36; 64 rows of 131072, k = 20, 28, 26 and 28.
+int row_splits(int T, int V) {
   const int most = (V + 8 * kThreads - 1) / (8 * kThreads);
-  int wg = k ? 1024 : 2048;
-  if (const char* e = getenv("LP_WG")) wg = atoi(e);
-  return std::max(1, std::min({most, wg / T, kMaxSplits}));
+  return std::max(1, std::min({most, 1024 / T, kMaxSplits}));
 }
 
 bool bad_sizes(const moe_logprob_args* a) {
@@ -628,7 +627,7 @@ bool bad_sizes(const moe_logprob_args* a) {
 
 extern "C" size_t moe_logprobs_workspace_size(const moe_logprob_args* a) {
   if (!a || a->T < 1 || bad_sizes(a)) return 0;
-  const size_t n = row_splits(a->T, a->V, a->k);
+  const size_t n = row_splits(a->T, a->V);
   return n == 1 ? 0 : (size_t)a->T * n * (sizeof(Piece) + (a->k ? 64 * 8 : 0));
 }
 
@@ -656,7 +655,7 @@ extern "C" moe_status moe_logprobs(const moe_logprob_args* a, moe_stream_t strea
                        need);
     MOE_CHECK_ARG(((uintptr_t)a->workspace & 15) == 0, "moe_logprobs: workspace must lie on a 16-byte boundary");
   }
-  const int splits = row_splits(a->T, a->V, a->k);
+  const int splits = row_splits(a->T, a->V);
   // whole 16-byte loads a piece, as far as the row's start allows
   const int piece = ((a->V + splits - 1) / splits + 7) / 8 * 8;
   const LogprobParams P{a->T, a->V, a->logits, ld, a->scale, (float)((double)a->scale * 1.44269504088896340736), a->ids,
