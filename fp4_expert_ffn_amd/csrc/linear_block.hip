@@ -18,13 +18,15 @@ using namespace moe;
 // Few rows: a stream of the weights, as k_linear_small.  One workgroup: NC
 // columns (gated: their gate and up rows) x 16 rows of one expert (of the
 // batch); its NWV waves take runs of kU K-steps in turn and load a run at
-// once.
-constexpr int kU = 4;
+// once: long runs where a wave has one, short ones, and so more waves a CU,
+// where there are many workgroups (16 tokens by 8 of 128 experts, 2048 x 768,
+// 21.8 us against 32.7 with runs of 4).
+constexpr int small_run(bool grouped) { return grouped ? 2 : 4; }
 
 template <bool GATED, bool EXACT, bool GROUPED, int NC, int NWV>
 __global__ __launch_bounds__(64 * NWV) void k_block_small(BlockParams B, int n_tiles) {
   static_assert(NC == 16 || (NC == 8 && GATED), "whole fragments");
-  constexpr int NB = GATED && NC == 16 ? 2 : 1;
+  constexpr int NB = GATED && NC == 16 ? 2 : 1, kU = small_run(GROUPED);
   __shared__ float part[NWV][NB][256];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n0 = (int)(blockIdx.x % n_tiles) * NC;
@@ -47,10 +49,12 @@ __global__ __launch_bounds__(64 * NWV) void k_block_small(BlockParams B, int n_t
   const uint8_t* wp[NB];
   wp[0] = P.w + (int64_t)n * P.ldw + g * 16;
   if constexpr (NB == 2) wp[1] = P.w + (int64_t)(P.N + n) * P.ldw + g * 16;
-  // scales: the lane's token; the tile's column block (gate's and up's, uniform)
+  // scales: the lane's token; the column block of its rows of each fragment
+  // (a lane of 32 .. 63 holds up rows where a fragment holds both)
   const float* xs = static_cast<const float*>(P.xs) + t;
-  const float* ws = static_cast<const float*>(P.ws) + (int64_t)(n0 >> 7) * B.steps;
-  const int64_t up = (int64_t)B.nb * B.steps;
+  const float* ws[NB];
+  ws[0] = static_cast<const float*>(P.ws) + (int64_t)((n0 >> 7) + (NC == 8 && g >= 2 ? B.nb : 0)) * B.steps;
+  if constexpr (NB == 2) ws[1] = ws[0] + (int64_t)B.nb * B.steps;
   lf32x4_t acc[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) acc[b] = lf32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -62,30 +66,29 @@ __global__ __launch_bounds__(64 * NWV) void k_block_small(BlockParams B, int n_t
   };
   for (int s0 = wave * kU; s0 < B.steps; s0 += NWV * kU) {
     Frag fx[kU], fw[kU][NB];
-    float sx[kU], sw[kU][2];
+    float sx[kU], sw[kU][NB];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int s = min(s0 + u, B.steps - 1);  // past the end: loaded, not used
+      const int s = min(s0 + u, B.steps - 1);  // past the end: the last step again, times 0
       fx[u] = load(xp, s);
-#pragma unroll
-      for (int b = 0; b < NB; ++b) fw[u][b] = load(wp[b], s);
       sx[u] = xs[(int64_t)s * B.X];
-      sw[u][0] = ws[s];
-      sw[u][1] = GATED ? ws[up + s] : 0.f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        fw[u][b] = load(wp[b], s);
+        sw[u][b] = ws[b][s];
+      }
     }
+    __builtin_amdgcn_sched_barrier(0);  // or the compiler waits for each step's loads before the next's
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      if (s0 + u < B.steps) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          lf32x4_t p = lf32x4_t{0.f, 0.f, 0.f, 0.f};
-          if constexpr (EXACT) p = mma_decoded<false>(fw[u][b], fx[u], p, 0, 0, g);
-          else p = mma_fp8<0, 0>(fw[u][b], fx[u], p, 127, 127);
-          // NC = 8: lanes 32 .. 63 hold the up rows
-          const float f = sx[u] * (NB == 2 ? sw[u][b] : (GATED && g >= 2 ? sw[u][1] : sw[u][0]));
+      for (int b = 0; b < NB; ++b) {
+        lf32x4_t p = lf32x4_t{0.f, 0.f, 0.f, 0.f};
+        if constexpr (EXACT) p = mma_decoded<false>(fw[u][b], fx[u], p, 0, 0, g);
+        else p = mma_fp8<0, 0>(fw[u][b], fx[u], p, 127, 127);
+        const float f = s0 + u < B.steps ? sx[u] * sw[u][b] : 0.f;
 #pragma unroll
-          for (int v = 0; v < 4; ++v) acc[b][v] = fmaf(p[v], f, acc[b][v]);
-        }
+        for (int v = 0; v < 4; ++v) acc[b][v] = fmaf(p[v], f, acc[b][v]);
       }
     }
   }
@@ -109,20 +112,46 @@ __global__ __launch_bounds__(64 * NWV) void k_block_small(BlockParams B, int n_t
   put(P, to, c, e.finish(P, a, u));
 }
 
-template <bool GATED, bool EXACT, bool GROUPED, int NC>
+template <bool GATED, bool EXACT, bool GROUPED, int NC, int NWV>
 void launch_small_waves(const BlockParams& B, hipStream_t s) {
   const int nt = (B.L.N + NC - 1) / NC;
   const long long rb = GROUPED ? most_row_blocks(B.L.T, B.E, 16) : (B.L.T + 15) / 16;
-  const dim3 g((unsigned)(nt * rb));
-  if (B.steps > 8 * kU) launch(k_block_small<GATED, EXACT, GROUPED, NC, 16>, g, dim3(1024), 0, s, B, nt);
-  else if (B.steps > 4 * kU) launch(k_block_small<GATED, EXACT, GROUPED, NC, 8>, g, dim3(512), 0, s, B, nt);
-  else launch(k_block_small<GATED, EXACT, GROUPED, NC, 4>, g, dim3(256), 0, s, B, nt);
+  launch(k_block_small<GATED, EXACT, GROUPED, NC, NWV>, dim3((unsigned)(nt * rb)), dim3(64 * NWV), 0, s, B, nt);
+}
+
+// Waves of a workgroup.  Dense: as many as have a run each.  Grouped: there are
+// workgroups enough, and the small ones end and start soonest.  us with 4, 8, 16
+// waves: 128 rows of 128 experts of 2 x 768 x 2048 33.4, 42.0, 53.1; 8 of 32
+// of 2 x 1024 x 7168 27.1, 25.6, 25.0; 32 of 128 of 2 x 1024 x 4096 35.8, 34.4,
+// 41.0.
+template <bool GATED, bool EXACT, bool GROUPED, int NC>
+void launch_small_cols(const BlockParams& B, hipStream_t s) {
+  if constexpr (GROUPED) {
+    if (B.steps >= 32) launch_small_waves<GATED, EXACT, GROUPED, NC, 8>(B, s);
+    else launch_small_waves<GATED, EXACT, GROUPED, NC, 4>(B, s);
+  } else {
+    constexpr int kU = small_run(false);
+    if (B.steps > 8 * kU) launch_small_waves<GATED, EXACT, GROUPED, NC, 16>(B, s);
+    else if (B.steps > 4 * kU) launch_small_waves<GATED, EXACT, GROUPED, NC, 8>(B, s);
+    else launch_small_waves<GATED, EXACT, GROUPED, NC, 4>(B, s);
+  }
+}
+
+template <bool GATED, bool GROUPED, bool EXACT>
+void launch_small_rows(const BlockParams& B, hipStream_t s) {
+  if constexpr (GATED && !GROUPED) {
+    // 8 gate and 8 up rows a workgroup by the linear product's rule: 2 x 2048 x
+    // 7168, one token, 6.9 us against 9.6.  Grouped it gained nothing (2 experts
+    // of 2 x 1024 x 4096 13.0 against 11.9).
+    if (eight_columns(std::min(B.L.T, 16), B.L.N, B.L.kb)) return launch_small_cols<GATED, EXACT, GROUPED, 8>(B, s);
+  }
+  launch_small_cols<GATED, EXACT, GROUPED, 16>(B, s);
 }
 
 template <bool GATED, bool GROUPED>
 void launch_small_out(const BlockParams& B, hipStream_t s) {
-  if (B.L.out_f32) launch_small_waves<GATED, true, GROUPED, 16>(B, s);
-  else launch_small_waves<GATED, false, GROUPED, 16>(B, s);
+  if (B.L.out_f32) launch_small_rows<GATED, GROUPED, true>(B, s);
+  else launch_small_rows<GATED, GROUPED, false>(B, s);
 }
 
 template <bool GROUPED>

@@ -33,19 +33,24 @@ inline TilePlan plan_block_tiles(int T, int N, bool gated, int K, bool exact) {
   return pl;
 }
 
-// Grouped: k_block_small while the experts have few rows each.
-inline bool grouped_small_wins(int T, int E) { return T <= 16 * E; }
+// Grouped: k_block_small while the experts have a row or two each.  us against
+// the better of the tiles, 128 experts of 2 x 768 x 2048: 64 rows 22.0 to 22.8,
+// 128 33.4 to 37.6, 512 61.2 to 62.2; of 2048 x 768: 128 23.3 to 22.3, 512
+// 44.1 to 40.3; 32 experts of 2 x 1024 x 7168: 32 rows 49 to 62.
+inline bool grouped_small_wins(int T, int E) { return T <= 2 * E; }
 
 // Else tiles walked without a pause: where the experts start and end is known
 // on the device alone, and each tile's look for its own place, its first loads
 // and its epilogue would stand still a CU's half.  us, 4096 tokens by 8 of 128
 // experts: 2 x 768 x 2048 180 against 207 with a workgroup a tile, 2048 x 768
 // 112 against 149; 512 tokens, 2 x 768 x 2048 93 against 97 (64 x 128 tiles).
+// Up to 8 rows an expert 64 x 128 tiles, which are more: 128 tokens 77 against
+// 82, 32 tokens 55 against 58, 64 tokens by 8 of 32 experts 24 against 28.
 // most: the most row blocks of 128 there can be.
 inline TilePlan plan_grouped_tiles(int T, int E, int N, bool gated, int K, bool exact, int64_t most) {
   const int steps = K / 128;
   const int64_t tiles = most * (gated ? (N + 63) / 64 : (N + 127) / 128);
-  if (!exact && steps >= 2 && tiles <= (int64_t)2 * kCus * kStreamTiles) return TilePlan{kStream, 1, steps};
+  if (!exact && T > 8 * E && steps >= 2 && tiles <= (int64_t)2 * kCus * kStreamTiles) return TilePlan{kStream, 1, steps};
   return TilePlan{T / E >= 48 ? 2 : 3, 1, steps};
 }
 
