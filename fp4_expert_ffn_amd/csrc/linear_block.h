@@ -95,7 +95,7 @@ struct TilePlan;
 // The tile kernel (linear_block_tile.hip).  False: the call's strides do not fit it.
 bool block_tile_fits(const BlockParams& B);
 void launch_block_tile(const BlockParams& B, const TilePlan& pl, void* workspace, hipStream_t s);
-// Tiles of 256 x 256 (linear_block_big.hip): bf16 outputs, K not split.
+// Tiles of 256 x 256 (linear_block_big.hip): dense, bf16 outputs, K not split.
 void launch_block_big(const BlockParams& B, hipStream_t s);
 // Tiles of 128 x 128 walked by two workgroups a CU (linear_block_stream.hip):
 // bf16 outputs, K not split and at least two blocks, at most kStreamTiles tiles a workgroup.

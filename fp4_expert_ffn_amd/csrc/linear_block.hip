@@ -21,12 +21,14 @@ using namespace moe;
 // once: long runs where a wave has one, short ones, and so more waves a CU,
 // where there are many workgroups (16 tokens by 8 of 128 experts, 2048 x 768,
 // 21.8 us against 32.7 with runs of 4).
-constexpr int small_run(bool grouped) { return grouped ? 2 : 4; }
+// Two fragments of weights a step leave no registers for runs of 4 beside 16
+// waves.
+constexpr int small_run(bool grouped, int fragments) { return grouped || fragments == 2 ? 2 : 4; }
 
 template <bool GATED, bool EXACT, bool GROUPED, int NC, int NWV>
 __global__ __launch_bounds__(64 * NWV) void k_block_small(BlockParams B, int n_tiles) {
   static_assert(NC == 16 || (NC == 8 && GATED), "whole fragments");
-  constexpr int NB = GATED && NC == 16 ? 2 : 1, kU = small_run(GROUPED);
+  constexpr int NB = GATED && NC == 16 ? 2 : 1, kU = small_run(GROUPED, NB);
   __shared__ float part[NWV][NB][256];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n0 = (int)(blockIdx.x % n_tiles) * NC;
@@ -119,7 +121,7 @@ void launch_small_waves(const BlockParams& B, hipStream_t s) {
   launch(k_block_small<GATED, EXACT, GROUPED, NC, NWV>, dim3((unsigned)(nt * rb)), dim3(64 * NWV), 0, s, B, nt);
 }
 
-// Waves of a workgroup.  Dense: as many as have a run each.  Grouped: there are
+// Waves of a workgroup.  Dense: as many as have a run of 2 to 4 each.  Grouped: there are
 // workgroups enough, and the small ones end and start soonest.  us with 4, 8, 16
 // waves: 128 rows of 128 experts of 2 x 768 x 2048 33.4, 42.0, 53.1; 8 of 32
 // of 2 x 1024 x 7168 27.1, 25.6, 25.0; 32 of 128 of 2 x 1024 x 4096 35.8, 34.4,
@@ -130,9 +132,8 @@ void launch_small_cols(const BlockParams& B, hipStream_t s) {
     if (B.steps >= 32) launch_small_waves<GATED, EXACT, GROUPED, NC, 8>(B, s);
     else launch_small_waves<GATED, EXACT, GROUPED, NC, 4>(B, s);
   } else {
-    constexpr int kU = small_run(false);
-    if (B.steps > 8 * kU) launch_small_waves<GATED, EXACT, GROUPED, NC, 16>(B, s);
-    else if (B.steps > 4 * kU) launch_small_waves<GATED, EXACT, GROUPED, NC, 8>(B, s);
+    if (B.steps > 32) launch_small_waves<GATED, EXACT, GROUPED, NC, 16>(B, s);
+    else if (B.steps > 16) launch_small_waves<GATED, EXACT, GROUPED, NC, 8>(B, s);
     else launch_small_waves<GATED, EXACT, GROUPED, NC, 4>(B, s);
   }
 }

@@ -31,7 +31,7 @@ namespace moe {
 
 namespace {
 
-template <bool GATED, bool GROUPED>
+template <bool GATED>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_block_big(BlockParams B, LinTiles G) {
   constexpr int WM = 2, WN = 4, TM = 8, TN = 4, BM = 256, BN = 256;
   constexpr int BO = GATED ? BN / 2 : BN;
@@ -39,27 +39,19 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   constexpr uint32_t kScales = 5 * 256;                      // a step's scales: 256 rows, 16 groups of weight rows
   __shared__ __align__(1024) uint8_t ring[2 * kStage];
   __shared__ __align__(256) uint8_t s_sc[3 * kScales];
-  LinParams P = B.L;
+  const LinParams P = B.L;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN, r16 = lane & 15, g = lane >> 4, lr = lane >> 3;
 
   // the tile: as in tile_product
-  int mt = G.mt;
-  if constexpr (GROUPED) mt = count_row_blocks<BM>(B);
+  const int mt = G.mt;
   const int total = mt * G.nt, per = (total + 7) / 8;
   if ((int)(blockIdx.x / 8) >= per) return;
   const int L = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
   if (L >= total) return;
   const int band = L / (4 * G.nt), in_band = L - band * 4 * G.nt, bh = min(4, mt - 4 * band);
   const int n0 = (in_band / bh) * BO;
-  int t0 = (4 * band + in_band % bh) * BM, t_end = P.T;
-  if constexpr (GROUPED) {
-    const RowBlock rb = find_row_block<BM>(B, 4 * band + in_band % bh);
-    t0 = rb.t0;
-    t_end = rb.end;
-    if (t0 >= t_end) return;
-    to_slot(B, rb.e, P);
-  }
+  const int t0 = (4 * band + in_band % bh) * BM, t_end = P.T;
   const int steps = B.steps;
   const uint32_t ring0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)ring;
   const uint32_t sc0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)s_sc;
@@ -71,7 +63,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   for (int u = 0; u < 4; ++u) {
     const int c = 4 * wave + u, j = 8 * c + lr;
     const int i = min(j, t_end - 1 - t0);
-    aoff[u] = (uint32_t)(GROUPED ? x_row(B, t0 + i) : i) * (uint32_t)P.ldx + piece(c) * 16;
+    aoff[u] = (uint32_t)i * (uint32_t)P.ldx + piece(c) * 16;
     const int col = GATED ? (j >> 5) * 16 + (j & 15) : j;
     boff[u] = (uint32_t)min(col, P.N - 1 - n0) * (uint32_t)P.ldw + piece(c) * 16;
   }
@@ -82,7 +74,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   int64_t sstep;
   if (sc < 4) {
     const int t = min(t0 + 64 * sc + lane, t_end - 1);
-    soff = (uint32_t)(GROUPED ? x_row(B, t) : t) * 4u;
+    soff = (uint32_t)t * 4u;
     ps = static_cast<const uint8_t*>(P.xs);
     sstep = (int64_t)B.X * 4;
   } else {
@@ -92,7 +84,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     ps = static_cast<const uint8_t*>(P.ws);
     sstep = 4;
   }
-  const uint8_t* pa = P.x + (GROUPED ? 0 : (int64_t)t0 * P.ldx);
+  const uint8_t* pa = P.x + (int64_t)t0 * P.ldx;
   const uint8_t* pb = P.w + (int64_t)n0 * P.ldw;
   // steps fa (x and scales) and fb (weights) are loaded next, into stage f % 2
   // and scale place f % 3; past the end the last step again
@@ -226,11 +218,10 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
                                                              wave);
 }
 
-template <bool GATED, bool GROUPED>
+template <bool GATED>
 void launch_one(const BlockParams& B, const LinTiles& G, hipStream_t s) {
-  const long long mt = GROUPED ? most_row_blocks(B.L.T, B.E, 256) : G.mt;
-  const long long grid = (mt * G.nt + 7) / 8 * 8;
-  launch(k_block_big<GATED, GROUPED>, dim3((unsigned)grid), dim3(512), 0, s, B, G);
+  const int64_t grid = ((int64_t)G.mt * G.nt + 7) / 8 * 8;
+  launch(k_block_big<GATED>, dim3((unsigned)grid), dim3(512), 0, s, B, G);
 }
 
 }  // namespace
@@ -240,11 +231,10 @@ void launch_block_big(const BlockParams& B, hipStream_t s) {
   LinTiles G{};
   G.mt = (P.T + 255) / 256;
   G.nt = P.gated ? (P.N + 127) / 128 : (P.N + 255) / 256;
-  G.vec_out = ((uintptr_t)P.out & 15) == 0 && (P.ldo * (P.out_f32 ? 4 : 2)) % 16 == 0;
+  G.vec_out = ((uintptr_t)P.out & 15) == 0 && (P.ldo * 2) % 16 == 0;
   G.vec_res = ((uintptr_t)P.res & 15) == 0 && P.ldr % 8 == 0;
   G.splits = 1;
-  if (B.offsets) P.gated ? launch_one<true, true>(B, G, s) : launch_one<false, true>(B, G, s);
-  else P.gated ? launch_one<true, false>(B, G, s) : launch_one<false, false>(B, G, s);
+  P.gated ? launch_one<true>(B, G, s) : launch_one<false>(B, G, s);
 }
 
 }  // namespace moe

@@ -68,7 +68,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   const int total = mt * G.nt, per = (total + 7) / 8;
   const int xcd = (int)(blockIdx.x % 8), w0 = (int)(blockIdx.x / 8), dealt = (int)(gridDim.x / 8);
   const int mine = min(per, total - xcd * per) - w0;
-  const int n = __builtin_amdgcn_readfirstlane(mine <= 0 ? 0 : (mine + dealt - 1) / dealt);  // at most kStreamTiles (the host's choice)
+  // at most kStreamTiles by the host's choice, whatever the offsets hold
+  const int n = __builtin_amdgcn_readfirstlane(mine <= 0 ? 0 : min((mine + dealt - 1) / dealt, kStreamTiles));
   if (n == 0) return;  // whole workgroups leave
   if (tid < n) {
     const int L = xcd * per + w0 + tid * dealt;

@@ -42,9 +42,11 @@ void launch_one(const BlockParams& B, const TilePlan& pl, float* part, hipStream
 
 template <bool GATED, bool EXACT, bool GROUPED>
 void launch_shape(const BlockParams& B, const TilePlan& pl, float* part, hipStream_t s) {
+  if constexpr (!GROUPED) {
+    if (pl.shape == 4) return launch_one<GATED, EXACT, GROUPED, 2, 1, 2, 4, 3>(B, pl, part, s);
+  }
   if (pl.shape == 2) launch_one<GATED, EXACT, GROUPED, 2, 2, 4, 4, 2>(B, pl, part, s);
-  else if (pl.shape == 3) launch_one<GATED, EXACT, GROUPED, 2, 2, 2, 4, 3>(B, pl, part, s);
-  else launch_one<GATED, EXACT, GROUPED, 2, 1, 2, 4, 3>(B, pl, part, s);
+  else launch_one<GATED, EXACT, GROUPED, 2, 2, 2, 4, 3>(B, pl, part, s);
 }
 
 template <bool GATED, bool GROUPED>
