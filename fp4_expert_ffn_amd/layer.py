@@ -231,6 +231,8 @@ class DenseLayer:
             return self.out[:0]
         if x.get_device() != self.out.get_device():
             raise L.MoeError(L.MOE_EINVAL, f"DenseLayer.forward: x is on {x.device}, the layer on {self.out.device}")
+        if tuple(x.shape) != (T, self.H):
+            raise L.MoeError(L.MOE_EINVAL, f"DenseLayer.forward: x has shape {tuple(x.shape)}, expected {(T, self.H)}")
         kept = x if residual is None else self.residual[:T]  # the sum that goes on
         for t, buf in ((x, self.out),) if residual is None else ((x, self.residual), (residual, self.residual)):
             if _other_rows(t, buf[:T]):
@@ -321,6 +323,15 @@ class BlockMoELayer:
             raise L.MoeError(L.MOE_EINVAL, f"BlockMoELayer.forward: x is on {x.device}, the layer on {self.out.device}")
         if x.shape[1] != H or x.stride(1) != 1:
             raise L.MoeError(L.MOE_EINVAL, f"BlockMoELayer.forward: x has shape {tuple(x.shape)}, expected dense rows of {H}")
+        t = L._Taken("BlockMoELayer.forward")  # what the calls below take as addresses
+        t("x", x, L._BF16, (T, H))
+        t.dense("logits", logits, L._F32, (T, self.E))
+        t.dense("w_router", w_router, L._F32, (self.E, H))
+        if logits is None and w_router is None:
+            raise L.MoeError(L.MOE_EINVAL, "BlockMoELayer.forward: neither logits nor w_router")
+        if rows is not None:
+            t.dense("rows[0]", rows[0], L._E4M3, (T, H))
+            t.dense("rows[1]", rows[1], L._F32, (H // 128, T))
         if logits is None:
             if not x.is_contiguous():
                 raise L.MoeError(L.MOE_EINVAL, "BlockMoELayer.forward: the router's product needs a contiguous x")
@@ -416,6 +427,8 @@ class TokenHead:
         if T > 0:
             if x.get_device() != self.logits.get_device():
                 raise L.MoeError(L.MOE_EINVAL, f"TokenHead.forward: x is on {x.device}, the head on {self.logits.device}")
+            if tuple(x.shape) != (T, self.H):
+                raise L.MoeError(L.MOE_EINVAL, f"TokenHead.forward: x has shape {tuple(x.shape)}, expected {(T, self.H)}")
             rows = ({"q": self.q.data_ptr(), "q_scale": self.q_scale.data_ptr(), "qmode": self.fmt}
                     if self.fmt != "bf16" else {"out": self.n.data_ptr()})
             L.moe_rmsnorm(L.norm_args(x=x, weight=self.norm_weight, eps=self.eps, residual=residual, **rows), stream)
