@@ -613,8 +613,12 @@ void launch_logprob(const LogprobParams& P, hipStream_t s) {
 
 // Pieces of a row: about four workgroups a CU, none with less than 8 logits a
 // thread.  us with 512, 1024 and 2048 workgroups: 333 rows of 50021 fp32 logits,
-// k = 5, 36, 33 and 36; 64 rows of 131072, k = 20, 28, 26 and 28.
+// k = 5, 36, 33 and 36; 64 rows of 131072, k = 20, 28, 26 and 28.  Up to 32
+// logits a thread the join's launch costs more than pieces save, us cut and
+// whole: 1 row of 4000, k = 1, 9.7 and 6.2; 128 rows of 8000, k = 20, 14.4 and
+// 13.4; 1 row of 16000, k = 1, 10.1 and 11.4.
 int row_splits(int T, int V) {
+  if (V <= 32 * kThreads) return 1;
   const int most = (V + 8 * kThreads - 1) / (8 * kThreads);
   return std::max(1, std::min({most, 1024 / T, kMaxSplits}));
 }
