@@ -17,7 +17,8 @@
 // largest, later the best k-th best of the workgroup's waves.  When 3 k have
 // gathered, the upper 16 bits of the k-th are found bit by bit with ballots,
 // become the bar, and what lies below goes: whatever the order of the logits, a
-// key is looked at a few times.  Only the row's last 64 are sorted.
+// key is looked at a few times.  Only the row's last 64 are sorted.  The best
+// alone (k = 1) needs none of it: a thread remembers where its maximum stood.
 //
 // Ranks are counted by ballots, on the scalar unit, and only where some lane's
 // largest reaches the given logit.
@@ -50,7 +51,7 @@ struct LogprobParams {
   int32_t* top_ids;
   float* top_logprob;
   int splits, piece;  // logits a piece
-  uint8_t* ws;        // splits > 1: [T * splits] Piece, then with k [T * splits][64] keys
+  uint8_t* ws;        // splits > 1: [T * splits] Piece, then keys: [T * splits][64], one each with k = 1
 };
 
 // What a piece of a row leaves: its maximum, the two sums against b, and the
@@ -297,11 +298,12 @@ constexpr float kHuge = 1e8f, kLeast = -1e8f;
 
 // The outputs of a row from its joined sums against b, by the whole workgroup
 // of NT threads: lane l of wave 0 holds the l-th best key.
-template <bool F32, int NT>
+// ONE: the best alone is wanted; 0 where no logit is above -inf.
+template <bool F32, bool ONE, int NT>
 __device__ __forceinline__ void finish_row(const LogprobParams& P, int t, const void* row, Given gt, float m, float b,
                                            double s0, double s1, int rank, uint64_t best) {
   __shared__ double s_sum[NT / 64][2];
-  __shared__ int s_nan;
+  __shared__ int s_nan, s_low;
   const int tid = threadIdx.x;
   const bool endless = !(fabsf(m) < __builtin_inff());
   const double mc = (double)m * (double)P.c;
@@ -312,19 +314,25 @@ __device__ __forceinline__ void finish_row(const LogprobParams& P, int t, const 
     s1 = f * (s1 + d * s0);
     s0 = f * s0;
   } else {  // uniform: the sums once more.  An endless m: tokens equal to it share the row
-    if (tid == 0) s_nan = 0;
+    if (tid == 0) {
+      s_nan = 0;
+      s_low = P.V;
+    }
     __syncthreads();
     double a0 = 0, a1 = 0;
     bool bad = false;
+    int low = P.V;  // the first logit equal to m
     for (int i = tid; i < P.V; i += NT) {
       const float v = logit<F32>(row, i);
       bad = bad || v != v;
+      if (ONE && v == m) low = min(low, i);
       const double d = v == m ? 0.0 : (endless ? -2000.0 : fmax((double)P.c * (double)v - mc, -2000.0));
       const double e = d <= -2000.0 ? 0.0 : exp2(d);
       a0 += e;
       a1 += d * e;
     }
     if (bad) atomicOr(&s_nan, 1);
+    if (ONE) atomicMin(&s_low, low);
     a0 = wave_sum64(a0);
     a1 = wave_sum64(a1);
     if ((tid & 63) == 0) {
@@ -333,6 +341,7 @@ __device__ __forceinline__ void finish_row(const LogprobParams& P, int t, const 
     }
     __syncthreads();
     nan = s_nan != 0;
+    if (ONE && best == 0u) best = s_low < P.V ? key_of(m, s_low) : key_of(__builtin_nanf(""), 0);
     s0 = s1 = 0;
     for (int w = 0; w < NT / 64; ++w) {
       s0 += s_sum[w][0];
@@ -369,10 +378,26 @@ __device__ __forceinline__ void join_wave(float& m, float& b, double& s0, double
   s1 = wave_sum64(s1);
 }
 
+// The wave's largest key, in every lane.
+__device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
+  auto larger = [](uint64_t a, uint64_t b) { return a > b ? a : b; };
+  v = larger(v, lane_xor64<1>(v));
+  v = larger(v, lane_xor64<2>(v));
+  v = larger(v, lane_xor64<7>(v));
+  v = larger(v, lane_xor64<15>(v));
+  v = larger(v, lane_xor64<16>(v));
+  return larger(v, lane_xor64<32>(v));
+}
+
+// What of the k best a call wants.
+enum { kNoTop, kBest, kList };
+
 // A workgroup: one piece of one row.  A thread takes 8 logits at a time.
-template <bool F32, bool TOP>
+template <bool F32, int WANT>
 __global__ __launch_bounds__(kThreads) void k_logprob(LogprobParams P) {
   constexpr int E = 8, ES = F32 ? 4 : 2, NL = F32 ? 2 : 1;
+  constexpr bool TOP = WANT == kList;
+  __shared__ uint64_t s_best[kWaves];
   __shared__ uint64_t s_keys[TOP ? kWaves : 1][kKeys], s_bar;
   __shared__ int s_held[kWaves];
   __shared__ double s_sum[kWaves][2];
@@ -398,7 +423,8 @@ __global__ __launch_bounds__(kThreads) void k_logprob(LogprobParams P) {
   const int shift = (int)(((uintptr_t)row & 15) / ES);
   const int q0 = (lo + shift) / E, q1 = (hi + shift + E - 1) / E;
   float m = -__builtin_inff(), b = kLeast, s0 = 0.f, s1 = 0.f;
-  int rank = 0;                 // uniform
+  int rank = 0;  // uniform
+  int mq = 0;    // kBest: the piece of 8 that m is from
   Keys keys(s_keys[TOP ? wave : 0], P.k, P.piece <= 16 * E * kThreads ? 64 : 8);
   auto whole = [&](int q) { return q < q1 && q * E - shift >= lo && q * E - shift + E <= hi; };
   auto load = [&](int q, uint4 (&u)[NL]) __attribute__((always_inline)) {
@@ -438,6 +464,7 @@ __global__ __launch_bounds__(kThreads) void k_logprob(LogprobParams P) {
     for (int j = 1; j < E; ++j) top = fmaxf(top, v[j]);
     if (top > m) {
       m = top;
+      if (WANT == kBest) mq = q;
       const float to = fmaxf(m * P.c, kLeast), d = fmaxf(b - to, -200.f), f = __builtin_amdgcn_exp2f(d);
       s1 = f * fmaf(d, s0, s1);
       s0 = f * s0;
@@ -504,6 +531,18 @@ __global__ __launch_bounds__(kThreads) void k_logprob(LogprobParams P) {
       for (int i = from + wave * 64; i < to; i += kThreads)  // uniform
         rank += __popcll(__ballot(i + lane < to && logit<F32>(row, min(i + lane, to - 1)) == gv));
   }
+  if constexpr (WANT == kBest) {  // the first of the 8 that equals m
+    int at = hi;
+    if (m > -__builtin_inff()) {
+#pragma unroll
+      for (int j = E - 1; j >= 0; --j) {
+        const int i = min(max(mq * E - shift + j, lo), hi - 1);
+        at = logit<F32>(row, i) == m ? i : at;
+      }
+    }
+    const uint64_t key = wave_max64(at < hi ? key_of(m, at) : 0u);
+    if (lane == 0) s_best[wave] = key;
+  }
   // the waves' sums
   double d0 = s0, d1 = s1;
   join_wave(m, b, d0, d1);
@@ -535,21 +574,27 @@ __global__ __launch_bounds__(kThreads) void k_logprob(LogprobParams P) {
   if constexpr (TOP) {
     if (wave == 0) best = keys.gather(s_held, &s_bar);
   }
+  if constexpr (WANT == kBest) {  // in every lane
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) best = s_best[w] > best ? s_best[w] : best;
+  }
   if (P.splits == 1) {
     if (TOP && wave == 0) best = sort64(best, keys.held);
-    finish_row<F32, kThreads>(P, t, row, gt, gm, gb, g0, g1, gr, best);
+    finish_row<F32, WANT == kBest, kThreads>(P, t, row, gt, gm, gb, g0, g1, gr, best);
     return;
   }
   if (tid == 0) reinterpret_cast<Piece*>(P.ws)[blockIdx.x] = Piece{g0, g1, gm, gb, gr, keys.held};
-  if (TOP && tid < keys.held)  // wave 0's
-    reinterpret_cast<uint64_t*>(P.ws + (int64_t)P.T * P.splits * sizeof(Piece))[(int64_t)blockIdx.x * 64 + tid] = best;
+  uint64_t* left = reinterpret_cast<uint64_t*>(P.ws + (int64_t)P.T * P.splits * sizeof(Piece));
+  if (TOP && tid < keys.held) left[(int64_t)blockIdx.x * 64 + tid] = best;  // wave 0's
+  if (WANT == kBest && tid == 0) left[blockIdx.x] = best;
 }
 
 // A workgroup: one row from its pieces, at most kMaxSplits.  Every wave joins
 // the sums (lane l: piece l) and takes every fourth piece's best.
 constexpr int kMaxSplits = 64;
-template <bool F32, bool TOP>
+template <bool F32, int WANT>
 __global__ __launch_bounds__(kThreads) void k_logprob_join(LogprobParams P) {
+  constexpr bool TOP = WANT == kList;
   __shared__ uint64_t s_keys[TOP ? kWaves : 1][kKeys], s_bar;
   __shared__ int s_held[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), t = blockIdx.x;
@@ -559,9 +604,10 @@ __global__ __launch_bounds__(kThreads) void k_logprob_join(LogprobParams P) {
   Piece p{0, 0, -__builtin_inff(), kLeast, 0, 0};
   if (lane < P.splits) p = pc[lane];
   uint64_t best = 0;
+  const uint64_t* left = reinterpret_cast<const uint64_t*>(P.ws + (int64_t)P.T * P.splits * sizeof(Piece));
+  if constexpr (WANT == kBest) best = wave_max64(lane < P.splits ? left[(int64_t)t * P.splits + lane] : 0u);
   if constexpr (TOP) {
-    const uint64_t* src = reinterpret_cast<const uint64_t*>(P.ws + (int64_t)P.T * P.splits * sizeof(Piece)) +
-                          (int64_t)t * P.splits * 64 + lane;
+    const uint64_t* src = left + (int64_t)t * P.splits * 64 + lane;
     if (tid == 0) s_bar = 0;
     __syncthreads();
     Keys keys(s_keys[wave], P.k, 64);
@@ -602,13 +648,20 @@ __global__ __launch_bounds__(kThreads) void k_logprob_join(LogprobParams P) {
   int rank = p.rank;
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) rank += __shfl_xor(rank, d);
-  finish_row<F32, kThreads>(P, t, row, gt, m, b, s0, s1, rank, best);
+  finish_row<F32, WANT == kBest, kThreads>(P, t, row, gt, m, b, s0, s1, rank, best);
 }
 
-template <bool F32, bool TOP>
+template <bool F32, int WANT>
+void launch_want(const LogprobParams& P, hipStream_t s) {
+  launch(k_logprob<F32, WANT>, dim3((unsigned)((int64_t)P.T * P.splits)), dim3(kThreads), 0, s, P);
+  if (P.splits > 1) launch(k_logprob_join<F32, WANT>, dim3((unsigned)P.T), dim3(kThreads), 0, s, P);
+}
+
+template <bool F32>
 void launch_logprob(const LogprobParams& P, hipStream_t s) {
-  launch(k_logprob<F32, TOP>, dim3((unsigned)((int64_t)P.T * P.splits)), dim3(kThreads), 0, s, P);
-  if (P.splits > 1) launch(k_logprob_join<F32, TOP>, dim3((unsigned)P.T), dim3(kThreads), 0, s, P);
+  if (P.k > 1) launch_want<F32, kList>(P, s);
+  else if (P.k == 1) launch_want<F32, kBest>(P, s);
+  else launch_want<F32, kNoTop>(P, s);
 }
 
 // Pieces of a row: about four workgroups a CU, none with less than 8 logits a
@@ -632,7 +685,7 @@ bool bad_sizes(const moe_logprob_args* a) {
 extern "C" size_t moe_logprobs_workspace_size(const moe_logprob_args* a) {
   if (!a || a->T < 1 || bad_sizes(a)) return 0;
   const size_t n = row_splits(a->T, a->V);
-  return n == 1 ? 0 : (size_t)a->T * n * (sizeof(Piece) + (a->k ? 64 * 8 : 0));
+  return n == 1 ? 0 : (size_t)a->T * n * (sizeof(Piece) + (a->k > 1 ? 64 * 8 : 8 * a->k));
 }
 
 extern "C" moe_status moe_logprobs(const moe_logprob_args* a, moe_stream_t stream) {
@@ -666,8 +719,7 @@ extern "C" moe_status moe_logprobs(const moe_logprob_args* a, moe_stream_t strea
                         a->logprob, a->rank, a->entropy, a->lse, a->k, a->top_ids, a->top_logprob, splits, piece,
                         static_cast<uint8_t*>(a->workspace)};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (a->logits_f32) top ? launch_logprob<true, true>(P, s) : launch_logprob<true, false>(P, s);
-  else top ? launch_logprob<false, true>(P, s) : launch_logprob<false, false>(P, s);
+  a->logits_f32 ? launch_logprob<true>(P, s) : launch_logprob<false>(P, s);
   MOE_LAUNCHED();
   return MOE_OK;
 }

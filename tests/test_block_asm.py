@@ -99,7 +99,7 @@ def test_walked_tiles(asm):
 
 @pytest.mark.parametrize("name,prefix,n", [("linear_block", "k_block_small", 26), ("linear_block_tile", "k_block_tile", 20),
                                            ("linear_block_big", "k_block_big", 2), ("linear_block_stream", "k_block_stream", 4),
-                                           ("logprob", "k_logprob", 8)])
+                                           ("logprob", "k_logprob", 12)])
 def test_no_scratch_and_no_flat_accesses(asm, name, prefix, n):
     code = kernels_of(asm(name), prefix)
     assert len(code) == n, sorted(code)

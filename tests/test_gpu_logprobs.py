@@ -174,6 +174,28 @@ def test_logprobs_masked_rows(m, V, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("V", [1, 300, 8192, 8193, 40000])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_logprobs_best_alone(m, V, dtype):
+    """k = 1: the first of equal largest logits, +0 and -0 among them, wherever they stand; rows cut and whole, and
+    pieces of a row that are masked throughout."""
+    need_gpu()
+    kind = torch.bfloat16 if dtype == "bf16" else torch.float32
+    for T in (1, 3, 700):
+        l = torch.full((T, V), -1.0)
+        l[0] = 0.0
+        l[0, ::2] = -0.0
+        for t in range(1, min(T, 50)):
+            l[t, t * 37 % V:] = 2.5
+        if T > 60:
+            l[50:60] = -math.inf
+            for t in range(51, 60):
+                l[t, t * 797 % V] = -3.0 * t
+        for shift, pad in ((0, 0), (1, 3)):
+            run(m, l.to(kind), 1.0, tokens(T, V), 1, pad=pad, shift=shift)
+
+
+@pytest.mark.gpu
 def test_logprobs_huge_and_tiny(m):
     """Logits over the whole range of their type; a nearly certain row; scales from 1e-3 to 1e3."""
     need_gpu()
