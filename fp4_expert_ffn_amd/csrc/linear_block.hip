@@ -15,7 +15,9 @@ namespace {
 
 using namespace moe;
 
-// Few rows: a stream of the weights, as k_linear_small.  One workgroup: NC
+// Few rows: a stream of the weights, as k_linear_small.  Bound: HBM, or where
+// few workgroups fill the call one memory latency.  1 x (2 x 2048) x 7168 6.8
+// us, 4.3 TB/s; 8 experts of it 42, 5.6 TB/s; 16 x 7168 x 2048 6.2.  One workgroup: NC
 // columns (gated: their gate and up rows) x 16 rows of one expert (of the
 // batch); its NWV waves take runs of kU K-steps in turn and load a run at
 // once: long runs where a wave has one, short ones, and so more waves a CU,

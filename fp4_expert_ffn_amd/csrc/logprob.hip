@@ -23,6 +23,12 @@
 // Ranks are counted by ballots, on the scalar unit, and only where some lane's
 // largest reaches the given logit.
 //
+// Bound: HBM on long batches, 4096 rows of 131072 bf16 logits (1.07 GB), k = 1,
+// 205 us, 5.2 TB/s; else latency and the instructions of the lists: 333 rows of
+// 50021 fp32 (67 MB), most masked, k = 5, 24 us and 7 for the join; one row of
+// 131072, k = 20, 7.4 and 6.  The lists of few keys wait on LDS, ballots and
+// cold instructions: sorting instead took 269 us where this took 212.
+//
 // Rows whose c m is beyond 1e8, infinite ones among them, or that hold a NaN,
 // are summed once more, in 64 bits (finish_row).
 #include <algorithm>

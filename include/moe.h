@@ -463,7 +463,8 @@ typedef struct {
  * [page "FreeToken量子化：MoE推論のセットアップガイド", 2nd paragraph: each
  *  token passes through only a few of the experts; block-scaled FP8 rows are
  *  this library's reading.]
- * Requires what moe_linear does, and x_rows * ldx below 2^32 bytes. */
+ * Requires what moe_linear does, x_rows * ldx below 2^32 bytes and strides of
+ * w and out below 2^24. */
 moe_status moe_linear_grouped(const moe_grouped_args* a, moe_stream_t stream);
 
 /* ------------------------------------------------------ log probabilities */
