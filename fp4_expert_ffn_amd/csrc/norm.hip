@@ -12,8 +12,8 @@
 // x 7168, bf16 residual in and out, MXFP8 out (826 MB): 145 us, 5.7 TB/s; a
 // copy of 1 GiB reaches 5.0.  1027 x 2048, fp32 residual, FP8 and bf16 out (27
 // MB): 7.8 us.  One row of 7168: 2.5 us, one of 64 2.1.  A scale per 128
-// columns: 16 lanes hold a block, its maximum is four DPP steps; one row of 7168 with residual 3.3 us, the encoding of 32768 x 2048 (203
-// MB) 40, 5.1 TB/s.
+// columns: 16 lanes hold a block, its maximum is four DPP steps; one row of
+// 7168 with residual 3.3 us, the encoding of 32768 x 2048 (203 MB) 40, 5.1 TB/s.
 #include <algorithm>
 
 #include "common.h"
