@@ -15,16 +15,16 @@ namespace {
 
 using namespace moe;
 
-// Few rows: a stream of the weights, as k_linear_small.  Bound: HBM, or where
-// few workgroups fill the call one memory latency.  1 x (2 x 2048) x 7168 6.8
-// us, 4.3 TB/s; 8 experts of it 42, 5.6 TB/s; 16 x 7168 x 2048 6.2.  One workgroup: NC
+// Few rows: a stream of the weights, as k_linear_small.  One workgroup: NC
 // columns (gated: their gate and up rows) x 16 rows of one expert (of the
 // batch); its NWV waves take runs of kU K-steps in turn and load a run at
 // once: long runs where a wave has one, short ones, and so more waves a CU,
 // where there are many workgroups (16 tokens by 8 of 128 experts, 2048 x 768,
-// 21.8 us against 32.7 with runs of 4).
-// Two fragments of weights a step leave no registers for runs of 4 beside 16
-// waves.
+// 21.8 us against 32.7 with runs of 4) or where two fragments of weights a step
+// leave no registers beside 16 waves.
+// Bound: HBM, or where few workgroups fill the call one memory latency.  1 x
+// (2 x 2048) x 7168 6.8 us, 4.3 TB/s; 8 experts of it 42, 5.6 TB/s; 16 x 7168
+// x 2048 6.2.
 constexpr int small_run(bool grouped, int fragments) { return grouped || fragments == 2 ? 2 : 4; }
 
 template <bool GATED, bool EXACT, bool GROUPED, int NC, int NWV>
