@@ -530,12 +530,12 @@ __global__ __launch_bounds__(kThreads) void k_logprob(LogprobParams P) {
     take(q + lane, v, first);
   }
   if constexpr (TOP) keys.publish(s_held, &s_bar, wave);
-  if (given) {  // equal logits of the 8 that hold the given one; of -inf all
+  if (given) {
+    // equal logits of the 8 that hold the given one, which may lie in two pieces: in each those that are its own; of -inf all
     const bool least = gv == -__builtin_inff();
     const int to = min(id, hi), from = least ? lo : max((id + shift) / E * E - shift, lo);
-    if (least || (id >= lo && id < hi))
-      for (int i = from + wave * 64; i < to; i += kThreads)  // uniform
-        rank += __popcll(__ballot(i + lane < to && logit<F32>(row, min(i + lane, to - 1)) == gv));
+    for (int i = from + wave * 64; i < to; i += kThreads)  // uniform
+      rank += __popcll(__ballot(i + lane < to && logit<F32>(row, min(i + lane, to - 1)) == gv));
   }
   if constexpr (WANT == kBest) {  // the first of the 8 that equals m
     int at = hi;
