@@ -85,12 +85,6 @@ __device__ __forceinline__ void to_slot(const BlockParams& B, int e, LinParams& 
   if (P.bias) P.bias += s * P.R;
 }
 
-// Most row blocks of BM rows that T rows of E experts can make.
-inline long long most_row_blocks(int T, int E, int bm) {
-  const long long used = T < E ? T : E;
-  return used + (T - used) / bm;
-}
-
 struct TilePlan;
 // The tile kernel (linear_block_tile.hip).  False: the call's strides do not fit it.
 bool block_tile_fits(const BlockParams& B);

@@ -119,19 +119,15 @@ __global__ __launch_bounds__(64 * NWV) void k_block_small(BlockParams B, int n_t
 template <bool GATED, bool EXACT, bool GROUPED, int NC, int NWV>
 void launch_small_waves(const BlockParams& B, hipStream_t s) {
   const int nt = (B.L.N + NC - 1) / NC;
-  const long long rb = GROUPED ? most_row_blocks(B.L.T, B.E, 16) : (B.L.T + 15) / 16;
+  const int64_t rb = GROUPED ? most_row_blocks(B.L.T, B.E, 16) : (B.L.T + 15) / 16;
   launch(k_block_small<GATED, EXACT, GROUPED, NC, NWV>, dim3((unsigned)(nt * rb)), dim3(64 * NWV), 0, s, B, nt);
 }
 
-// Waves of a workgroup.  Dense: as many as have a run of 2 to 4 each.  Grouped: there are
-// workgroups enough, and the small ones end and start soonest.  us with 4, 8, 16
-// waves: 128 rows of 128 experts of 2 x 768 x 2048 33.4, 42.0, 53.1; 8 of 32
-// of 2 x 1024 x 7168 27.1, 25.6, 25.0; 32 of 128 of 2 x 1024 x 4096 35.8, 34.4,
-// 41.0.
+// Waves of a workgroup.  Dense: as many as have a run of 2 to 4 each.
 template <bool GATED, bool EXACT, bool GROUPED, int NC>
 void launch_small_cols(const BlockParams& B, hipStream_t s) {
   if constexpr (GROUPED) {
-    if (B.steps >= 32) launch_small_waves<GATED, EXACT, GROUPED, NC, 8>(B, s);
+    if (grouped_small_waves(B.L.K) == 8) launch_small_waves<GATED, EXACT, GROUPED, NC, 8>(B, s);
     else launch_small_waves<GATED, EXACT, GROUPED, NC, 4>(B, s);
   } else {
     if (B.steps > 32) launch_small_waves<GATED, EXACT, GROUPED, NC, 16>(B, s);
@@ -229,8 +225,7 @@ extern "C" moe_status moe_linear_grouped(const moe_grouped_args* g, moe_stream_t
   const BlockParams B{{a->T, a->N, a->K, R, a->K, static_cast<const uint8_t*>(a->x), static_cast<const uint8_t*>(a->w),
                        ldx, ldw, a->x_scale, a->w_scale, a->bias, nullptr, a->out, 0, ldo, a->fn, a->gated, a->out_f32},
                       g->x_rows, steps, nb, g->E, g->rows_div, g->offsets, g->rows, g->slot_of_expert, wst, sst / 4};
-  // a workgroup for every 16 columns and row block at most: what a grid holds
-  MOE_CHECK_ARG(most_row_blocks(a->T, g->E, 16) * ((a->N + 15) / 16) < (1LL << 22),
+  MOE_CHECK_ARG(grouped_threads(a->T, g->E, a->N, a->gated, a->K, a->out_f32, block_tile_fits(B)) < (1LL << 32),
                 "moe_linear_grouped: T=%d rows of N=%d are more than a grid holds", a->T, a->N);
   launch_linear_block(B, nullptr, reinterpret_cast<hipStream_t>(stream));
   MOE_LAUNCHED();

@@ -33,6 +33,12 @@ inline TilePlan plan_block_tiles(int T, int N, bool gated, int K, bool exact) {
   return pl;
 }
 
+// Most row blocks of bm rows that T rows of E experts can make.
+inline int64_t most_row_blocks(int T, int E, int bm) {
+  const int64_t used = T < E ? T : E;
+  return used + (T - used) / bm;
+}
+
 // Grouped: k_block_small while the experts have a row or two each.  us against
 // the better of the tiles, 128 experts of 2 x 768 x 2048: 64 rows 22.0 to 22.8,
 // 128 33.4 to 37.6, 512 61.2 to 62.2; of 2048 x 768: 128 23.3 to 22.3, 512
@@ -52,6 +58,22 @@ inline TilePlan plan_grouped_tiles(int T, int E, int N, bool gated, int K, bool 
   const int64_t tiles = most * (gated ? (N + 63) / 64 : (N + 127) / 128);
   if (!exact && T > 8 * E && steps >= 2 && tiles <= (int64_t)2 * kCus * kStreamTiles) return TilePlan{kStream, 1, steps};
   return TilePlan{T / E >= 48 ? 2 : 3, 1, steps};
+}
+
+// Waves of a grouped k_block_small workgroup: there are workgroups enough, and the small ones end and start
+// soonest.  us with 4, 8, 16 waves: 128 rows of 128 experts of 2 x 768 x 2048 33.4, 42.0, 53.1; 8 of 32 of 2 x
+// 1024 x 7168 27.1, 25.6, 25.0; 32 of 128 of 2 x 1024 x 4096 35.8, 34.4, 41.0.
+inline int grouped_small_waves(int K) { return K / 128 >= 32 ? 8 : 4; }
+
+// Threads of the grid that a grouped call launches; a grid holds fewer than
+// 2^32.  fits: the call's strides fit the tiles.
+inline int64_t grouped_threads(int T, int E, int N, bool gated, int K, bool exact, bool fits) {
+  if (!fits || grouped_small_wins(T, E))
+    return most_row_blocks(T, E, 16) * ((N + 15) / 16) * 64 * grouped_small_waves(K);
+  const TilePlan pl = plan_grouped_tiles(T, E, N, gated, K, exact, most_row_blocks(T, E, 128));
+  if (pl.shape == kStream) return (int64_t)2 * kCus * 256;
+  const int bo = kShapes[pl.shape].bn / (gated ? 2 : 1);
+  return (most_row_blocks(T, E, kShapes[pl.shape].bm) * ((N + bo - 1) / bo) + 7) / 8 * 8 * 256;
 }
 
 }  // namespace moe

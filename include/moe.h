@@ -463,8 +463,10 @@ typedef struct {
  * [page "FreeToken量子化：MoE推論のセットアップガイド", 2nd paragraph: each
  *  token passes through only a few of the experts; block-scaled FP8 rows are
  *  this library's reading.]
- * Requires what moe_linear does, x_rows * ldx below 2^32 bytes and strides of
- * w and out below 2^24. */
+ * Requires what moe_linear does, x_rows * ldx below 2^32 bytes, strides of w
+ * and out below 2^24, and a grid of fewer than 2^32 threads: 256 take 64 x 64
+ * outputs at least, or up to 512 16 x 16 where rows of x lie 2^24 bytes apart
+ * (batches that pass it are refused). */
 moe_status moe_linear_grouped(const moe_grouped_args* a, moe_stream_t stream);
 
 /* ------------------------------------------------------ log probabilities */
