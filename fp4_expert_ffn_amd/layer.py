@@ -271,7 +271,8 @@ class BlockMoELayer:
     Weights: gate_up [S, 2 I, H] (the I gate rows, then the I up rows) with fp32 scales [S, 2 ceil(I / 128),
     H / 128], down [S, H, I] with [S, ceil(H / 128), I / 128], in S slots; slot_of_expert int32 [E] maps expert
     to slot (None: slot e).  shared: None, or (gate_up, gate_up_scale, down, down_scale) of the always-on expert,
-    without the slots' dimension.  router as in MoELayer.
+    without the slots' dimension.  router as in MoELayer.  E up to 1024, k up to min(E, 16), I up to 32768, and H
+    where forward encodes x; a call's T below 65536, T * k up to 131072 and T * k * I below 2^32.
 
     Every call writes the layer's own buffers: one layer serves one stream at a time, and the next call replaces
     what the last returned."""
@@ -280,6 +281,9 @@ class BlockMoELayer:
                  shared=None, router=None, renormalize=True, device="cuda"):
         if H % 128 or I % 128:
             raise L.MoeError(L.MOE_EINVAL, f"BlockMoELayer: H and I in multiples of 128 (H={H}, I={I})")
+        if not (1 <= E <= 1024 and 1 <= k <= min(E, 16) and H > 0 and 0 < I <= 32768):
+            raise L.MoeError(L.MOE_EINVAL, f"BlockMoELayer: bad sizes E={E} k={k} H={H} I={I} (E up to 1024, k up to "
+                                           f"min(E, 16), I up to 32768)")
         dev, T = torch.device(device), max(max_tokens, 1)
         self.E, self.k, self.H, self.I, self.max_tokens = E, k, H, I, T
         self.gate_up, self.gate_up_scale, self.down, self.down_scale = gate_up, gate_up_scale, down, down_scale
@@ -319,6 +323,11 @@ class BlockMoELayer:
         assert T <= self.max_tokens
         if T == 0:
             return self.out[:0]
+        if T >= 65536 or T * k > 131072 or T * k * I >= 1 << 32:  # what the calls below serve
+            raise L.MoeError(L.MOE_EINVAL, f"BlockMoELayer.forward: T={T} by k={k} of I={I} (T below 65536, T * k up to "
+                                           f"131072, T * k * I below 2^32)")
+        if rows is None and H > 32768:
+            raise L.MoeError(L.MOE_EINVAL, f"BlockMoELayer.forward: H={H}, up to 32768 are encoded (rows is None)")
         if x.get_device() != self.out.get_device():
             raise L.MoeError(L.MOE_EINVAL, f"BlockMoELayer.forward: x is on {x.device}, the layer on {self.out.device}")
         if x.shape[1] != H or x.stride(1) != 1:
