@@ -341,6 +341,7 @@ class BlockMoELayer:
         if rows is not None:
             t.dense("rows[0]", rows[0], L._E4M3, (T, H))
             t.dense("rows[1]", rows[1], L._F32, (H // 128, T))
+        L._current(t, "BlockMoELayer.forward")
         if logits is None:
             if not x.is_contiguous():
                 raise L.MoeError(L.MOE_EINVAL, "BlockMoELayer.forward: the router's product needs a contiguous x")

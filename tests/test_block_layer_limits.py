@@ -1,7 +1,8 @@
 """What BlockMoELayer cannot serve is refused before any of its calls is made
-(CPU: no device is touched), at its construction where no batch could be
-served."""
+(no kernel runs here), at its construction where no batch could be served."""
 import pytest
+
+from tests.gpu_util import DEV, need_gpu
 
 torch = pytest.importorskip("torch")
 
@@ -60,3 +61,16 @@ def test_rows_too_long_for_the_encoder(m, made):
 
 def test_largest_sizes_are_taken(m):
     assert layer(E=1024, k=16, H=32768, I=32768, max_tokens=1).k == 16
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("own_logits", [False, True])
+def test_another_device_than_the_current_one(m, made, monkeypatch, own_logits):
+    """The router's calls take addresses: the layer itself sees that its tensors lie where the stream runs."""
+    need_gpu()
+    lay = layer(device=DEV)
+    x, w = torch.zeros((2, 128), dtype=torch.bfloat16, device=DEV), torch.zeros((4, 128), device=DEV)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(m.MoeError) as e:
+        lay.forward(x, stream=0, **(dict(logits=w[:2, :4].contiguous()) if own_logits else dict(w_router=w)))
+    assert e.value.status == 1 and "current device cuda:1" in str(e.value) and not made, made
