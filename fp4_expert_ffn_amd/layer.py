@@ -383,7 +383,7 @@ class TokenHead:
         logits = norm(x + residual) W^T;  then moe_logprobs of scale * logits
 
     fmt and w [V,H], w_scale as DenseLayer's weights ("bf16", "fp8", "mxfp8", "fp8_block"); logits fp32
-    (logits_f32) or bf16; k alternatives a row.  Every call writes the head's own buffers: one head serves one
+    (logits_f32) or bf16; k alternatives a row, up to min(64, V).  Every call writes the head's own buffers: one head serves one
     stream at a time, and the next call replaces what the last returned."""
 
     def __init__(self, *, H, V, fmt, max_tokens, norm_weight, w, w_scale=None, k=0, eps=1e-6, logits_f32=False,
@@ -391,6 +391,8 @@ class TokenHead:
         dev, T = torch.device(device), max(max_tokens, 1)
         if fmt in _BLOCKED and H % 128:
             raise L.MoeError(L.MOE_EINVAL, f"TokenHead: {fmt} rows need H in multiples of 128 (H={H})")
+        if not (1 <= V < 1 << 24 and 0 <= k <= min(64, V)):
+            raise L.MoeError(L.MOE_EINVAL, f"TokenHead: bad sizes V={V} k={k} (V below 2^24, k up to min(64, V))")
         self.H, self.V, self.fmt, self.k, self.eps, self.max_tokens = H, V, fmt, k, eps, T
         self.norm_weight, self.w, self.w_scale = norm_weight, w, w_scale
         new = lambda *n, t=torch.float32: torch.empty(n, dtype=t, device=dev)  # noqa: E731
@@ -441,9 +443,14 @@ class TokenHead:
                 raise L.MoeError(L.MOE_EINVAL, f"TokenHead.forward: x has shape {tuple(x.shape)}, expected {(T, self.H)}")
             rows = ({"q": self.q.data_ptr(), "q_scale": self.q_scale.data_ptr(), "qmode": self.fmt}
                     if self.fmt != "bf16" else {"out": self.n.data_ptr()})
-            L.moe_rmsnorm(L.norm_args(x=x, weight=self.norm_weight, eps=self.eps, residual=residual, **rows), stream)
-            L.moe_linear(self._linear(T), stream)
-            L.moe_logprobs(self._logprobs(T, ids, scale), stream)
+            # every argument is looked at before the first call is enqueued
+            norm = L.norm_args(x=x, weight=self.norm_weight, eps=self.eps, residual=residual, **rows)
+            product, answer = self._linear(T), self._logprobs(T, ids, scale)
+            if not 0.0 < answer.scale < float("inf"):
+                raise L.MoeError(L.MOE_EINVAL, f"TokenHead.forward: scale must be positive and finite, not {scale}")
+            L.moe_rmsnorm(norm, stream)
+            L.moe_linear(product, stream)
+            L.moe_logprobs(answer, stream)
         return {n: getattr(self, n)[:T] for n in names}
 
 
