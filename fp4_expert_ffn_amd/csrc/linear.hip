@@ -33,7 +33,7 @@ __global__ __launch_bounds__(64 * NWV) void k_linear_small(LinParams P, int n_ti
   static_assert(NC == 16 || (NC == 8 && GATED), "whole fragments");
   constexpr int NB = GATED && NC == 16 ? 2 : 1;
   constexpr bool MX = QM == MOE_Q_MXFP8;
-  __shared__ float part[NWV][NB][256];
+  __shared__ __align__(16) float part[NWV][NB][256];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n0 = (int)(blockIdx.x % n_tiles) * NC, t0 = (int)(blockIdx.x / n_tiles) * 16;
   const int r = lane & 15, g = lane >> 4;

@@ -31,7 +31,7 @@ template <bool GATED, bool EXACT, bool GROUPED, int NC, int NWV>
 __global__ __launch_bounds__(64 * NWV) void k_block_small(BlockParams B, int n_tiles) {
   static_assert(NC == 16 || (NC == 8 && GATED), "whole fragments");
   constexpr int NB = GATED && NC == 16 ? 2 : 1, kU = small_run(GROUPED, NB);
-  __shared__ float part[NWV][NB][256];
+  __shared__ __align__(16) float part[NWV][NB][256];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n0 = (int)(blockIdx.x % n_tiles) * NC;
   LinParams P = B.L;

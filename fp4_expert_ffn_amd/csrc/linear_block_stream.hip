@@ -31,7 +31,7 @@ namespace moe {
 
 namespace {
 
-struct Tile {
+struct __align__(16) Tile {  // read in one 16-byte piece
   int t0, end, n0, slot;
 };
 
