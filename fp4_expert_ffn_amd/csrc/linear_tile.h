@@ -1,5 +1,5 @@
 // The body of the tile kernels of the linear product (linear_tile.hip,
-// linear_block.hip) and the join of a split K.
+// linear_block_tile.hip) and the join of a split K.
 #pragma once
 #include <type_traits>
 
@@ -14,7 +14,7 @@ namespace moe {
 // Direct global->LDS loads of a wave: lane l's 16 (4) bytes at base + off
 // land at dst + 16 l (4 l); dst is wave-uniform.  They write no register, and
 // the kernel orders them by its own counted waits.  The compiler uses M0
-// nowhere else in this kernel (a CPU test checks it).
+// nowhere else in the kernels that call them (CPU tests check it).
 __device__ __forceinline__ void dma16s(uint32_t off, const uint8_t* base, uint32_t dst) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(dst)
                : "memory", "m0");
@@ -246,7 +246,7 @@ __device__ __forceinline__ void tile_product(LinParams P, const LinTiles& G, con
   float nw[BLK ? 2 : 1], nx[BLK ? TH : 1];  // those of the next step, of the next half
   // sums of the last instructions, not added yet, and their scales: instruction
   // n of a half leaves its own in place n % kLate, whose former ones are added first
-  constexpr int kLate = TM > 4 || EXACT ? 2 : 4;
+  constexpr int kLate = EXACT ? 2 : 4;
   lf32x4_t late[BLK ? kLate : 1];
   float late_f[BLK ? kLate : 1];
   static_assert(!BLK || TN * TH % kLate == 0, "places go on from half to half");
@@ -594,7 +594,7 @@ __global__ __launch_bounds__(64 * WM* WN) __attribute__((amdgpu_waves_per_eu(2, 
   tile_product<QM, GATED, EXACT, false, WM, WN, TM, TN, S>(P, G, nullptr);
 }
 
-// Those with a scale per block of 128, dense and grouped (linear_block.hip).
+// Those with a scale per block of 128, dense and grouped (linear_block_tile.hip).
 template <bool GATED, bool EXACT, bool GROUPED, int WM, int WN, int TM, int TN, int S>
 __global__ __launch_bounds__(64 * WM* WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_block_tile(BlockParams B,
                                                                                                        LinTiles G) {
