@@ -12,8 +12,10 @@
 //
 // 4096 tokens by 8 of 128 experts: 2 x 768 x 2048 175 us (198 with a workgroup a
 // tile), 2048 x 768 112 (149).  Matrix cores 0.34 busy, texture unit 0.68, L2
-// hits 0.66, 692 MB fetched of 461 read once; with weights that the L2 holds
-// already 23 us less.
+// hits 0.66, 692 MB fetched of 411 read once: a band of four row tiles takes in
+// several experts, some 170 passes over an expert's weights for 128 of them; a
+// quarter of the matrix instructions is for empty rows of last tiles.  With
+// weights that the L2 holds already 23 us less.
 //
 // One step in four parts as in linear_block_big.hip, part i the wave's i-th 16
 // rows.  When a step starts, its weights and the first half of its x are in
